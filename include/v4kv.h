@@ -53,6 +53,7 @@ typedef int32_t v4kv_status;
 #define V4KV_DEV_TIMEOUT 16  /* a wait inside a kernel gave up (no progress) */
 #define V4KV_DEV_RANGE 32    /* a bf16 value beyond the f16 range met the     */
                              /* 64-head tensor-core path and was clamped      */
+#define V4KV_DEV_BAD_PROB 64 /* a row of probabilities with no finite, positive sum */
 
 typedef enum { V4KV_BF16 = 0, V4KV_FP8_E4M3 = 1, V4KV_FP32 = 2, V4KV_FP4_E2M1 = 3 } v4kv_dtype;
 
@@ -361,6 +362,134 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
                                           const int32_t* topk, int32_t k, float sm_scale,
                                           v4kv_rope rope, void* out, int32_t* dev_status,
                                           void* stream);
+
+/*
+ * Trees of drafted tokens (speculative decoding). A draft model proposes
+ * several next tokens per sequence as a tree; one pass of the target model
+ * attends every node at once (v4kv_tree_attention), v4kv_tree_verify accepts a
+ * path of them and v4kv_tree_gather packs the accepted rows for
+ * v4kv_compress_append. The pages have no counterpart: they describe decoding
+ * one token at a time.
+ *
+ * All three calls describe the trees the same way:
+ *   cu_nodes    device int32 [batch + 1], non-decreasing from 0: sequence b's
+ *               nodes are rows cu_nodes[b] .. cu_nodes[b+1] of every per-node
+ *               array (rows behind cu_nodes[batch] are neither read nor written)
+ *   total_nodes host: rows of the per-node arrays
+ *   max_nodes   host bound of a sequence's nodes, 1 .. V4KV_MAX_TREE_NODES; the
+ *               nodes of a longer sequence beyond it are left out and flagged
+ *               V4KV_DEV_OVERFLOW
+ *   parents     device int32 [total_nodes]: index within the sequence of the
+ *               node's parent, which comes before it; -1 for a root. A parent
+ *               that does not come before its child is flagged
+ *               V4KV_DEV_BAD_INDEX and the child taken as a root.
+ */
+#define V4KV_MAX_TREE_NODES 128
+
+/*
+ * v4kv_tree_attention -- decode attention of every drafted node. With L =
+ * seq_lens[b] tokens in the cache, node i sits at position pos = L + depth(i)
+ * (a root's depth is 0) and attends to
+ *   - entries j < floor(max(0, pos + 1 - window_len) / ratio) (topk == NULL),
+ *     or { topk[node][i] >= 0 },
+ *   - the cache's tokens t in [max(0, pos + 1 - window_len), L),
+ *   - its ancestors in the tree and itself,
+ * which is what v4kv_decode_attention gives after the path to the node has
+ * been appended. The drafted tokens' K = V rows are passed in k_tree, not in
+ * the cache (v4kv_qk_prepare with heads = 1 rotates them).
+ * Numerics: every operand of the tensor cores is one or two fp8-e4m3 terms.
+ * Cached codes are exact. A bf16 row (an entry, a window token, k_tree or q) is
+ * split into two terms relative to its largest magnitude A, exact for values
+ * of at least 2^-13 A and within 2^-22 A below; an fp32 q is
+ * rounded to such terms (relative 2^-9). Softmax weights are rounded to two
+ * terms (relative 2^-9) with a power-of-two scale per 32 items; accumulation,
+ * maxima and sums are fp32. Any fp8 scale is valid, zero and negative ones too.
+ * A row that is not attended never enters a result, whatever it holds; an
+ * attended row with a NaN or an infinity makes the attending outputs NaN (at
+ * least in the dims that hold it).
+ *   q           device [total_nodes, heads, dim], fp32 or bf16, RoPE applied at
+ *               each node's position
+ *   k_tree      device bf16 [total_nodes, dim], RoPE applied
+ *   window_len  at least max_nodes, so that no drafted token leaves the window
+ *   topk        device int32 [total_nodes, k] or NULL, k 1 .. 2048
+ *   out         device bf16 [total_nodes, heads, dim]
+ *   workspace   device scratch of v4kv_tree_workspace_size bytes, 256-byte
+ *               aligned; contents need not be initialised
+ * Everything else, and a node with nothing to attend to (zeros), is as in
+ * v4kv_decode_attention.
+ */
+v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, int32_t heads,
+                                const int32_t* cu_nodes, int32_t total_nodes, int32_t max_nodes,
+                                const int32_t* parents, const void* k_tree,
+                                const v4kv_paged* main_cache, const v4kv_paged* window,
+                                const int32_t* seq_lens, int32_t max_seq_len, int32_t ratio,
+                                int32_t window_len, const int32_t* topk, int32_t k, float sm_scale,
+                                v4kv_rope rope, void* out, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream);
+
+/* Scratch bytes of v4kv_tree_attention for the same arguments (host only;
+ * queries the current device's SM count; k is 0 when topk is NULL). */
+v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total_nodes,
+                                     int32_t max_nodes, int32_t max_seq_len, int32_t ratio,
+                                     int32_t window_len, int32_t k, int32_t main_dtype, size_t* bytes);
+
+/*
+ * v4kv_tree_verify -- accept a path of drafted tokens with given random
+ * numbers, so that accepted tokens and the next one follow the target's
+ * distribution. Node 0 of a sequence is the root, a token that is already
+ * certain. Starting there, the children of the last accepted node are asked in
+ * index order. With p the node's row of the target, q its row of the draft, x
+ * the child's token, u = accept_u[child], and r = p, R = 1 at first:
+ *   - accept the child when u * q(x) * R < r(x); its children come next;
+ *   - else r = max(r - R q, 0) elementwise and R = sum(r).
+ * Without a draft (NULL) the drafts are fixed guesses: q(x) = 1 in the test,
+ * and a refusal sets r(x) = 0 and R = R - r(x). When no child is left, the
+ * next token is the smallest i with r(0) + .. + r(i) > sample_u[b] * sum(r)
+ * (p instead of r when r has no positive value left). Products and sums are
+ * fp64 (the order of a sum is fixed); a value that is not positive counts as 0.
+ *   target      device [total_nodes, row_stride] of target_dtype (fp32 or
+ *               bf16), row i the distribution after node i; vocab values used
+ *   draft       the same of draft_dtype, row i the distribution node i's
+ *               children were drawn from, or NULL
+ *   row_stride  elements between rows, at least vocab
+ *   tokens      device int32 [total_nodes]; a child whose token is outside
+ *               [0, vocab) is flagged V4KV_DEV_BAD_INDEX and not accepted
+ *   accept_u    device fp32 [total_nodes], in [0, 1)
+ *   sample_u    device fp32 [batch], in [0, 1)
+ *   path_out    device int32 [batch, max_nodes]: accepted nodes (indices within
+ *               the sequence) from the root on, padded with -1
+ *   n_path_out  device int32 [batch]: how many, the root included
+ *   next_token  device int32 [batch]: -1 for a sequence without nodes, and,
+ *               flagged V4KV_DEV_BAD_PROB, when p has no finite positive sum
+ */
+v4kv_status v4kv_tree_verify(const void* target, int32_t target_dtype, const void* draft,
+                             int32_t draft_dtype, int32_t vocab, int64_t row_stride, int32_t batch,
+                             const int32_t* cu_nodes, int32_t total_nodes, int32_t max_nodes,
+                             const int32_t* parents, const int32_t* tokens, const float* accept_u,
+                             const float* sample_u, int32_t* path_out, int32_t* n_path_out,
+                             int32_t* next_token, int32_t* dev_status, void* stream);
+
+/*
+ * v4kv_tree_gather -- the accepted nodes' raw rows and gates, packed as
+ * v4kv_compress_append takes them (x, gate, cu_seqlens; seq_start is the L the
+ * trees were attended with, and L + n_path the next one). Row cu_out[b] + i is
+ * node path[b][i] of sequence b. Rows behind cu_out[batch] are left as they
+ * were, so x_out.rows may be passed as total_tokens without reading cu_out back.
+ *   x, gate       device bf16 [total_nodes, dim] and fp32 [total_nodes,
+ *                 gate_dim] (1, or dim for per-channel gates)
+ *   path, n_path  as written by v4kv_tree_verify (path rows of max_nodes)
+ *   x_out, gate_out  the same types, `capacity` rows; rows beyond it are dropped
+ *                 and flagged V4KV_DEV_OVERFLOW (cu_out never exceeds capacity);
+ *                 must not overlap x and gate
+ *   cu_out        device int32 [batch + 1]
+ * dim a multiple of 8 in [8, 1024]; gate and gate_out 16-byte aligned. A path
+ * index outside the sequence is flagged V4KV_DEV_BAD_INDEX and its row zeroed.
+ */
+v4kv_status v4kv_tree_gather(const void* x, const float* gate, int32_t dim, int32_t gate_dim,
+                             int32_t batch, const int32_t* cu_nodes, int32_t total_nodes,
+                             int32_t max_nodes, const int32_t* path, const int32_t* n_path,
+                             void* x_out, float* gate_out, int32_t capacity, int32_t* cu_out,
+                             int32_t* dev_status, void* stream);
 
 #define V4KV_OP_INDEX_TOPK 1
 #define V4KV_OP_DECODE 2

@@ -11,6 +11,7 @@ _EXPORTS = {
     "v4kv_decode_attention", "v4kv_decode_attention_fp8out", "v4kv_decode_attention_noalloc", "v4kv_index_topk",
     "v4kv_kv_footprint_bytes", "v4kv_slot_mapping", "v4kv_status_string", "v4kv_version",
     "v4kv_workspace_size", "v4kv_qk_prepare",
+    "v4kv_tree_attention", "v4kv_tree_workspace_size", "v4kv_tree_verify", "v4kv_tree_gather",
 }
 
 

@@ -80,6 +80,11 @@ bool rope_ok(const v4kv_rope& r, int dim) {
   return r.theta > 0.0 && isfinite(r.theta);
 }
 
+// what the three tree calls require of their common arguments
+bool tree_ok(int32_t batch, const int32_t* cu_nodes, int32_t total_nodes, int32_t max_nodes) {
+  return batch > 0 && cu_nodes && total_nodes >= 0 && max_nodes >= 1 && max_nodes <= V4KV_MAX_TREE_NODES;
+}
+
 RopeArgs to_rope(const v4kv_rope& r) {
   RopeArgs a{};
   a.theta = r.theta;
@@ -403,6 +408,143 @@ v4kv_status v4kv_decode_attention_fp8out(const void* q, int32_t q_dtype, int32_t
   return decode_impl(q, q_dtype, batch, heads, main_cache, window, seq_lens, max_seq_len, ratio,
                      window_len, topk, k, sm_scale, rope, out_codes, 1, out_scales, prequant_out,
                      workspace, workspace_bytes, dev_status, stream);
+}
+
+v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, int32_t heads,
+                                const int32_t* cu_nodes, int32_t total_nodes, int32_t max_nodes,
+                                const int32_t* parents, const void* k_tree,
+                                const v4kv_paged* main_cache, const v4kv_paged* window,
+                                const int32_t* seq_lens, int32_t max_seq_len, int32_t ratio,
+                                int32_t window_len, const int32_t* topk, int32_t k, float sm_scale,
+                                v4kv_rope rope, void* out, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream) {
+  if (!tree_ok(batch, cu_nodes, total_nodes, max_nodes)) return V4KV_ERR_INVALID_ARG;
+  if (total_nodes > 0 && (!parents || !k_tree || !aligned16(k_tree))) return V4KV_ERR_INVALID_ARG;
+  // no drafted token may leave the window: the entries it would belong to do not exist
+  if (window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
+  // the other arguments are checked as v4kv_decode_attention checks them (the
+  // per-node arrays of an empty call may be NULL)
+  const bool empty = total_nodes == 0;
+  v4kv_status st = decode_check_args(empty ? workspace : q, q_dtype, batch, heads, main_cache, window,
+                                     seq_lens, max_seq_len, ratio, window_len, topk, k, sm_scale, rope,
+                                     empty ? workspace : out);
+  if (st != V4KV_OK) return st;
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != V4KV_OK) return st;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < tree_workspace_bytes(batch, heads, total_nodes, max_nodes, sms))
+    return V4KV_ERR_INVALID_ARG;
+  if (empty) return V4KV_OK;
+  TreeArgs a{};
+  a.q = q;
+  a.cu_nodes = cu_nodes;
+  a.parents = parents;
+  a.k_tree = static_cast<const uint16_t*>(k_tree);
+  a.seq_lens = seq_lens;
+  a.topk = topk;
+  a.out = static_cast<uint16_t*>(out);
+  a.dev_status = dev_status;
+  a.main = to_args(main_cache);
+  a.window = to_args(window);
+  a.rope = to_rope(rope);
+  a.q_dtype = q_dtype;
+  a.batch = batch;
+  a.heads = heads;
+  a.total_nodes = total_nodes;
+  a.max_nodes = max_nodes;
+  a.max_len = max_seq_len;
+  a.ratio = ratio;
+  a.window_len = window_len;
+  a.k = topk ? k : 0;
+  a.sm_scale = sm_scale == 0.f ? 1.f / sqrtf(512.f) : sm_scale;
+  return to_status(launch_tree_attention(a, workspace, sms, (cudaStream_t)stream));
+}
+
+v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total_nodes,
+                                     int32_t max_nodes, int32_t max_seq_len, int32_t ratio,
+                                     int32_t window_len, int32_t k, int32_t main_dtype, size_t* bytes) {
+  (void)main_dtype;
+  if (!bytes || batch <= 0 || total_nodes < 0 || max_seq_len < 0 || k < 0) return V4KV_ERR_INVALID_ARG;
+  if (max_nodes < 1 || max_nodes > V4KV_MAX_TREE_NODES || window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
+  if (heads < 1 || heads > 128) return V4KV_ERR_UNSUPPORTED;
+  if (ratio != 4 && ratio != 128) return V4KV_ERR_INVALID_ARG;
+  int sms = 0;
+  v4kv_status st = check_device(&sms);
+  if (st != V4KV_OK) return st;
+  *bytes = tree_workspace_bytes(batch, heads, total_nodes, max_nodes, sms);
+  return V4KV_OK;
+}
+
+v4kv_status v4kv_tree_verify(const void* target, int32_t target_dtype, const void* draft,
+                             int32_t draft_dtype, int32_t vocab, int64_t row_stride, int32_t batch,
+                             const int32_t* cu_nodes, int32_t total_nodes, int32_t max_nodes,
+                             const int32_t* parents, const int32_t* tokens, const float* accept_u,
+                             const float* sample_u, int32_t* path_out, int32_t* n_path_out,
+                             int32_t* next_token, int32_t* dev_status, void* stream) {
+  if (!tree_ok(batch, cu_nodes, total_nodes, max_nodes)) return V4KV_ERR_INVALID_ARG;
+  if (!sample_u || !path_out || !n_path_out || !next_token) return V4KV_ERR_INVALID_ARG;
+  if (total_nodes > 0 && (!target || !parents || !tokens || !accept_u)) return V4KV_ERR_INVALID_ARG;
+  if (target_dtype != V4KV_FP32 && target_dtype != V4KV_BF16) return V4KV_ERR_INVALID_ARG;
+  if (draft && draft_dtype != V4KV_FP32 && draft_dtype != V4KV_BF16) return V4KV_ERR_INVALID_ARG;
+  if (vocab < 1 || row_stride < vocab) return V4KV_ERR_INVALID_ARG;
+  if ((target && !aligned16(target)) || (draft && !aligned16(draft))) return V4KV_ERR_INVALID_ARG;
+  v4kv_status st = check_device(nullptr);
+  if (st != V4KV_OK) return st;
+  VerifyArgs a{};
+  a.target = target;
+  a.draft = draft;
+  a.target_dtype = target_dtype;
+  a.draft_dtype = draft_dtype;
+  a.vocab = vocab;
+  a.row_stride = row_stride;
+  a.batch = batch;
+  a.cu_nodes = cu_nodes;
+  a.total_nodes = total_nodes;
+  a.max_nodes = max_nodes;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.accept_u = accept_u;
+  a.sample_u = sample_u;
+  a.path_out = path_out;
+  a.n_path_out = n_path_out;
+  a.next_token = next_token;
+  a.dev_status = dev_status;
+  return to_status(launch_tree_verify(a, (cudaStream_t)stream));
+}
+
+v4kv_status v4kv_tree_gather(const void* x, const float* gate, int32_t dim, int32_t gate_dim,
+                             int32_t batch, const int32_t* cu_nodes, int32_t total_nodes,
+                             int32_t max_nodes, const int32_t* path, const int32_t* n_path,
+                             void* x_out, float* gate_out, int32_t capacity, int32_t* cu_out,
+                             int32_t* dev_status, void* stream) {
+  if (!tree_ok(batch, cu_nodes, total_nodes, max_nodes)) return V4KV_ERR_INVALID_ARG;
+  if (!path || !n_path || !cu_out || capacity < 0) return V4KV_ERR_INVALID_ARG;
+  if (total_nodes > 0 && (!x || !gate)) return V4KV_ERR_INVALID_ARG;
+  if (capacity > 0 && (!x_out || !gate_out)) return V4KV_ERR_INVALID_ARG;
+  if (dim < 8 || dim > 1024 || dim % 8 || (gate_dim != 1 && gate_dim != dim)) return V4KV_ERR_INVALID_ARG;
+  if ((x && !aligned16(x)) || (x_out && !aligned16(x_out)) || (gate && !aligned16(gate)) ||
+      (gate_out && !aligned16(gate_out)))
+    return V4KV_ERR_INVALID_ARG;
+  v4kv_status st = check_device(nullptr);
+  if (st != V4KV_OK) return st;
+  GatherArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.gate = gate;
+  a.dim = dim;
+  a.gate_dim = gate_dim;
+  a.batch = batch;
+  a.cu_nodes = cu_nodes;
+  a.total_nodes = total_nodes;
+  a.max_nodes = max_nodes;
+  a.path = path;
+  a.n_path = n_path;
+  a.x_out = static_cast<uint16_t*>(x_out);
+  a.gate_out = gate_out;
+  a.capacity = capacity;
+  a.cu_out = cu_out;
+  a.dev_status = dev_status;
+  return to_status(launch_tree_gather(a, (cudaStream_t)stream));
 }
 
 uint64_t v4kv_kv_footprint_bytes(uint64_t n_tokens, const v4kv_footprint_cfg* c) {

@@ -139,6 +139,75 @@ struct DecodeArgs {
   float2* rope_tab;    // tensor-core path: [batch][kRopeTable] (cos, sin) at position L - 1
 };
 
+// drafted-token trees (tree_attend.cu, tree_verify.cu)
+struct TreeArgs {
+  const void* q;            // [total_nodes, heads, 512] fp32 or bf16
+  const int32_t* cu_nodes;  // [batch + 1]
+  const int32_t* parents;   // [total_nodes]
+  const uint16_t* k_tree;   // [total_nodes, 512] bf16
+  const int32_t* seq_lens;  // [batch] tokens in the cache
+  const int32_t* topk;      // [total_nodes, k] or null
+  uint16_t* out;            // [total_nodes, heads, 512] bf16
+  int32_t* dev_status;
+  PoolArgs main;
+  PoolArgs window;
+  RopeArgs rope;
+  int q_dtype;
+  int batch;
+  int heads;
+  int total_nodes;
+  int max_nodes;
+  int max_len;  // host bound on seq_lens; longer sequences are clamped and flagged
+  int ratio;
+  int window_len;
+  int k;
+  float sm_scale;
+};
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;  // or null: fixed guesses
+  int target_dtype;
+  int draft_dtype;
+  int vocab;
+  long long row_stride;
+  int batch;
+  const int32_t* cu_nodes;
+  int total_nodes;
+  int max_nodes;
+  const int32_t* parents;
+  const int32_t* tokens;
+  const float* accept_u;
+  const float* sample_u;
+  int32_t* path_out;
+  int32_t* n_path_out;
+  int32_t* next_token;
+  int32_t* dev_status;
+};
+
+struct GatherArgs {
+  const uint16_t* x;
+  const float* gate;
+  int dim;
+  int gate_dim;
+  int batch;
+  const int32_t* cu_nodes;
+  int total_nodes;
+  int max_nodes;
+  const int32_t* path;
+  const int32_t* n_path;
+  uint16_t* x_out;
+  float* gate_out;
+  int capacity;
+  int32_t* cu_out;
+  int32_t* dev_status;
+};
+
+cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
+size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int num_sms);
+cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_gather(const GatherArgs& a, cudaStream_t stream);
+
 cudaError_t launch_slot_mapping(const int32_t* bt, int max_blocks, int batch,
                                 const int32_t* seq_start, const int32_t* n_new, int ratio, int spb,
                                 int num_pages, int32_t* cu_out, int64_t* slot_out, long long cap,

@@ -25,6 +25,7 @@ V4KV_DEV_BAD_INDEX = 4
 V4KV_DEV_OVERFLOW = 8
 V4KV_DEV_TIMEOUT = 16
 V4KV_DEV_RANGE = 32
+V4KV_DEV_BAD_PROB = 64
 V4KV_BF16 = 0
 V4KV_FP8_E4M3 = 1
 V4KV_FP32 = 2
@@ -39,9 +40,11 @@ EXPORTED = [
     "v4kv_decode_attention_noalloc", "v4kv_decode_attention_fp8out",
     "v4kv_page_bytes", "v4kv_plan_buckets", "v4kv_page_pools_create", "v4kv_page_pools_destroy",
     "v4kv_page_alloc", "v4kv_page_free", "v4kv_pages_free",
+    "v4kv_tree_attention", "v4kv_tree_workspace_size", "v4kv_tree_verify", "v4kv_tree_gather",
 ]
 
 V4KV_NOALLOC_SCRATCH_BYTES = 32 << 20
+V4KV_MAX_TREE_NODES = 128
 
 
 class V4KVError(RuntimeError):
@@ -103,6 +106,12 @@ def _load():
         "v4kv_decode_attention_fp8out": (I32, [P, I32, I32, I32, ctypes.POINTER(_Paged),
                                                ctypes.POINTER(_Paged), P, I32, I32, I32, P, I32,
                                                F32, _Rope, P, P, P, P, SZ, P, P]),
+        "v4kv_tree_attention": (I32, [P, I32, I32, I32, P, I32, I32, P, P, ctypes.POINTER(_Paged),
+                                      ctypes.POINTER(_Paged), P, I32, I32, I32, P, I32, F32, _Rope, P, P,
+                                      SZ, P, P]),
+        "v4kv_tree_workspace_size": (I32, [I32] * 9 + [ctypes.POINTER(SZ)]),
+        "v4kv_tree_verify": (I32, [P, I32, P, I32, I32, I64, I32, P, I32, I32, P, P, P, P, P, P, P, P, P]),
+        "v4kv_tree_gather": (I32, [P, P, I32, I32, I32, P, I32, I32, P, P, P, P, I32, P, P, P]),
         "v4kv_workspace_size": (I32, [I32, I32, I32, I32, I32, I32, I32, I32, I32,
                                       ctypes.POINTER(SZ)]),
         "v4kv_kv_footprint_bytes": (ctypes.c_uint64, [ctypes.c_uint64, ctypes.POINTER(_Footprint)]),
@@ -369,6 +378,119 @@ def v4kv_decode_attention_noalloc(q, main, window, seq_lens, max_seq_len, ratio,
         _ptr(topk), topk.shape[1] if topk is not None else 0, sm_scale, rope.c(), out.data_ptr(),
         _ptr(dev_status), _stream(stream))
     _check("v4kv_decode_attention_noalloc", st)
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+
+def v4kv_tree_workspace_size(batch, heads, total_nodes, max_nodes, max_seq_len, ratio, window_len, k, main_dtype):
+    out = ctypes.c_size_t(0)
+    st = _lib.v4kv_tree_workspace_size(batch, heads, total_nodes, max_nodes, max_seq_len, ratio, window_len,
+                                       k, main_dtype, ctypes.byref(out))
+    _check("v4kv_tree_workspace_size", st)
+    return out.value
+
+
+def v4kv_tree_attention(q, cu_nodes, parents, k_tree, main, window, seq_lens, max_nodes, max_seq_len, ratio,
+                        window_len, out, workspace, topk=None, sm_scale=None, rope=None, dev_status=None,
+                        stream=None):
+    """Decode attention of every node of the sequences' drafted-token trees:
+    q and out [total_nodes, heads, 512], k_tree [total_nodes, 512] the nodes'
+    own rows, parents the index of each node's parent within its sequence."""
+    _need(q, (torch.float32, torch.bfloat16), "q", ndim=3)
+    _need(cu_nodes, (torch.int32,), "cu_nodes", ndim=1)
+    _need(parents, (torch.int32,), "parents", ndim=1)
+    _need(k_tree, (torch.bfloat16,), "k_tree", ndim=2)
+    _need(seq_lens, (torch.int32,), "seq_lens", ndim=1)
+    _need(out, (torch.bfloat16,), "out", ndim=3)
+    _need(workspace, (torch.uint8,), "workspace")
+    n = q.shape[0]
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if parents.shape[0] != n or tuple(k_tree.shape) != (n, q.shape[2]):
+        raise ValueError("parents and k_tree must have one row per node")
+    if cu_nodes.shape[0] != seq_lens.shape[0] + 1:
+        raise ValueError("cu_nodes must have one value more than seq_lens")
+    if topk is not None:
+        _need(topk, (torch.int32,), "topk", ndim=2)
+        if topk.shape[0] != n:
+            raise ValueError("topk must have one row per node")
+    rope = rope or Rope()
+    mc, wc = main.c(), window.c()
+    st = _lib.v4kv_tree_attention(
+        q.data_ptr(), V4KV_FP32 if q.dtype == torch.float32 else V4KV_BF16, seq_lens.shape[0], q.shape[1],
+        cu_nodes.data_ptr(), n, max_nodes, parents.data_ptr(), k_tree.data_ptr(), ctypes.byref(mc),
+        ctypes.byref(wc), seq_lens.data_ptr(), max_seq_len, ratio, window_len, _ptr(topk),
+        topk.shape[1] if topk is not None else 0, 0.0 if sm_scale is None else sm_scale, rope.c(),
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check("v4kv_tree_attention", st)
+
+
+def _row_stride(t, what):
+    if t is None:
+        raise ValueError(f"{what} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{what} has dtype {t.dtype}, expected float32 or bfloat16")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what} must be [nodes, vocab] with consecutive values in a row")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def v4kv_tree_verify(target, cu_nodes, parents, tokens, accept_u, sample_u, max_nodes, path_out, n_path_out,
+                     next_token, draft=None, dev_status=None, stream=None):
+    """Accept a path of drafted tokens per sequence: target (and draft)
+    [total_nodes, vocab] probabilities after each node, whose rows may be
+    further apart than vocab (both alike); path_out [batch, max_nodes]."""
+    stride = _row_stride(target, "target")
+    for t, name, dt in ((cu_nodes, "cu_nodes", torch.int32), (parents, "parents", torch.int32),
+                        (tokens, "tokens", torch.int32), (accept_u, "accept_u", torch.float32),
+                        (sample_u, "sample_u", torch.float32), (n_path_out, "n_path_out", torch.int32),
+                        (next_token, "next_token", torch.int32)):
+        _need(t, (dt,), name, ndim=1)
+    _need(path_out, (torch.int32,), "path_out", ndim=2)
+    n, vocab = target.shape
+    batch = cu_nodes.shape[0] - 1
+    if parents.shape[0] != n or tokens.shape[0] != n or accept_u.shape[0] != n:
+        raise ValueError("parents, tokens and accept_u must have one value per row of target")
+    if sample_u.shape[0] != batch or n_path_out.shape[0] != batch or next_token.shape[0] != batch or \
+            tuple(path_out.shape) != (batch, max_nodes):
+        raise ValueError("sample_u, n_path_out, next_token and path_out must have one row per sequence")
+    if draft is not None and (_row_stride(draft, "draft") != stride or draft.shape != target.shape):
+        raise ValueError("draft must have target's shape and row stride")
+    code = {torch.float32: V4KV_FP32, torch.bfloat16: V4KV_BF16}
+    st = _lib.v4kv_tree_verify(
+        target.data_ptr(), code[target.dtype], _ptr(draft), code[draft.dtype] if draft is not None else 0,
+        vocab, stride, batch, cu_nodes.data_ptr(), n, max_nodes, parents.data_ptr(), tokens.data_ptr(),
+        accept_u.data_ptr(), sample_u.data_ptr(), path_out.data_ptr(), n_path_out.data_ptr(),
+        next_token.data_ptr(), _ptr(dev_status), _stream(stream))
+    _check("v4kv_tree_verify", st)
+
+
+def v4kv_tree_gather(x, gate, cu_nodes, path, n_path, x_out, gate_out, cu_out, dev_status=None, stream=None):
+    """Pack the accepted nodes' rows and gates ([total_nodes] or
+    [total_nodes, dim]) for v4kv_compress_append (cu_out is its cu_seqlens)."""
+    _need(x, (torch.bfloat16,), "x", ndim=2)
+    _need(x_out, (torch.bfloat16,), "x_out", ndim=2)
+    _need(gate, (torch.float32,), "gate")
+    _need(gate_out, (torch.float32,), "gate_out")
+    _need(cu_nodes, (torch.int32,), "cu_nodes", ndim=1)
+    _need(path, (torch.int32,), "path", ndim=2)
+    _need(n_path, (torch.int32,), "n_path", ndim=1)
+    _need(cu_out, (torch.int32,), "cu_out", ndim=1)
+    dim = x.shape[1]
+    batch, max_nodes = path.shape
+    if x_out.shape[1] != dim or gate.dim() not in (1, 2) or gate_out.dim() != gate.dim() or \
+            gate.shape[0] != x.shape[0] or gate_out.shape[0] != x_out.shape[0] or \
+            (gate.dim() == 2 and (gate.shape[1] != dim or gate_out.shape[1] != dim)):
+        raise ValueError("gate must be [nodes] or [nodes, dim], and the outputs shaped like x and gate")
+    if n_path.shape[0] != batch or cu_nodes.shape[0] != batch + 1 or cu_out.shape[0] != batch + 1:
+        raise ValueError("path and n_path need one row per sequence, cu_nodes and cu_out one value more")
+    st = _lib.v4kv_tree_gather(x.data_ptr(), gate.data_ptr(), dim, 1 if gate.dim() == 1 else dim, batch,
+                               cu_nodes.data_ptr(), x.shape[0], max_nodes, path.data_ptr(), n_path.data_ptr(),
+                               x_out.data_ptr(), gate_out.data_ptr(), x_out.shape[0], cu_out.data_ptr(),
+                               _ptr(dev_status), _stream(stream))
+    _check("v4kv_tree_gather", st)
 
 
 def v4kv_kv_footprint_bytes(n_tokens, layer_ratios, dim, entry_bits, entry_scale_bytes=0,

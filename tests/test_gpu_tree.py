@@ -1,0 +1,632 @@
+"""Trees of drafted tokens on the GPU against the fp64 oracle: attention of
+every node, verification with given random numbers, packing of accepted rows,
+and one speculative step of all of them with the append."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import codecs, tree
+from tests.helpers import entry_rows, lay_out, window_rows
+
+pytestmark = pytest.mark.gpu
+
+W = 128
+
+
+def make_parents(r, n, shape):
+    if shape == "chain":
+        return [-1] + list(range(n - 1)) if n else []
+    if shape == "star":
+        return [-1] + [0] * (n - 1) if n else []
+    if shape == "forest":  # every node a root
+        return [-1] * n
+    return [-1 if i == 0 else int(r.integers(max(0, (i - 1) // 4), i)) for i in range(n)]
+
+
+class TreeCase:
+    def __init__(self, seed, lens, counts, heads, ratio=4, main_dtype="fp8", win_dtype="bf16", shape="tree",
+                 topk=0, window=W, spare=0, q_std=1.0):
+        r = synth.rng(seed)
+        self.lens, self.counts, self.H, self.ratio, self.W = list(lens), list(counts), heads, ratio, window
+        spb = 256 // ratio
+        ents = [entry_rows(r, -(-L // ratio), main_dtype) for L in lens]
+        ents = [e if e[0].shape[0] else (np.zeros((0, 512), e[0].dtype), e[1]) for e in ents]
+        self.main = lay_out(ents, spb, r, main_dtype,
+                            max_blocks=max([-(-(-(-L // ratio)) // spb) for L in lens] + [1]))
+        first = [max(0, L - window) // 256 for L in lens]
+        self.win = lay_out([window_rows(r, L, window, win_dtype) for L in lens], 256, r, win_dtype, first_block=first,
+                           max_blocks=max([-(-L // 256) for L in lens] + [1]))
+        self.cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        self.N = int(self.cu[-1]) + spare
+        self.parents = np.full(self.N, -1, dtype=np.int32)
+        for b, n in enumerate(counts):
+            self.parents[self.cu[b]:self.cu[b + 1]] = make_parents(r, n, shape)
+        self.q = codecs.bf16_round(synth.normal(r, (self.N, heads, 512), q_std))
+        self.k_tree = codecs.bf16_round(synth.normal(r, (self.N, 512)))
+        self.topk = None
+        if topk:
+            self.topk = np.full((self.N, topk), -1, dtype=np.int32)
+            for b, n in enumerate(counts):
+                vis = max(0, lens[b] + 1 - window) // ratio
+                for i in range(n):
+                    m = min(topk, vis)
+                    pick = np.sort(r.permutation(vis)[:m])
+                    at = np.sort(r.permutation(topk)[:m])
+                    self.topk[self.cu[b] + i, at] = pick
+        self.max_nodes = max(max(counts), 1)
+        self.max_len = max(lens)
+
+    def device(self, q_fp32=False):
+        d = {"main": self.main.to_cuda(), "win": self.win.to_cuda()}
+        d["q"] = torch.from_numpy(self.q).cuda() if q_fp32 else synth.bf16_tensor(self.q).cuda()
+        d["k_tree"] = synth.bf16_tensor(self.k_tree).cuda()
+        d["cu"] = torch.from_numpy(self.cu).cuda()
+        d["parents"] = torch.from_numpy(self.parents).cuda()
+        d["lens"] = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+        d["topk"] = torch.from_numpy(self.topk).cuda() if self.topk is not None else None
+        d["out"] = torch.full((self.N, self.H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        d["st"] = torch.zeros(1, dtype=torch.int32, device="cuda")
+        d["ws"] = self.workspace(d)
+        return d
+
+    def workspace(self, d):
+        from paged_compressed_kv_b200 import v4kv
+        n = v4kv.v4kv_tree_workspace_size(len(self.lens), self.H, self.N, self.max_nodes, self.max_len, self.ratio,
+                                          self.W, 0 if self.topk is None else self.topk.shape[1], d["main"].dtype_code)
+        # whatever an earlier call left there
+        return torch.randint(0, 256, (max(n, 256),), dtype=torch.uint8, device="cuda")
+
+    def run(self, d, stream=None, **kw):
+        from paged_compressed_kv_b200 import v4kv
+        v4kv.v4kv_tree_attention(d["q"], d["cu"], d["parents"], d["k_tree"], d["main"], d["win"], d["lens"],
+                                 self.max_nodes, self.max_len, self.ratio, self.W, d["out"], d["ws"],
+                                 topk=d["topk"], dev_status=d["st"], stream=stream, **kw)
+
+    def oracle(self, b, i):
+        lo = self.cu[b]
+        return tree.attend_node(self.q[lo + i], i, self.parents[lo:self.cu[b + 1]], self.k_tree[lo:self.cu[b + 1]],
+                                self.main.seq(b), self.win.seq(b), self.lens[b], self.ratio, self.W,
+                                1 / math.sqrt(512), topk_row=None if self.topk is None else self.topk[lo + i])
+
+    def check(self, out, nodes=None, q_fp32=False):
+        """Every value against fp64. A weight carries at most 2^-9 from its two
+        e4m3 terms (half a step of the second term of a value in [1, 2) is
+        2^-9) and the result one bf16 rounding (2^-8). With bf16 queries the
+        scores are sums of exact products; their fp32 accumulation, and that of
+        the outputs, stays below 2^-12 at these sizes (512 products a score of
+        magnitude below 8: 512 * 8 * 2^-24 / 2). An fp32 query adds 2^-9 of
+        sum|q v| scale, below 2^-9 * 16 here (|q||v| / sqrt(512) at the drawn
+        sizes), to each score, and twice that to a weight's ratio. A weight
+        below 2^-21 of its block's largest may vanish: 2^-16 of the largest
+        value covers any number of them here."""
+        out = out.float().cpu().numpy().astype(np.float64)
+        for b, n in enumerate(self.counts):
+            for i in range(n) if nodes is None else [i for i in nodes if i < n]:
+                ref, mass = self.oracle(b, i)
+                got = out[self.cu[b] + i]
+                tol = (2.0 ** -9 + 2.0 ** -11) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * np.abs(mass).max()
+                if q_fp32:
+                    tol += 2 * 2.0 ** -9 * 16 * mass
+                bad = np.abs(got - ref) > tol
+                assert not bad.any(), (b, i, np.abs(got - ref)[bad].max(), tol[bad].min(), int(bad.sum()))
+
+
+def chosen(c, r, most=6):
+    return sorted(set(int(x) for x in r.integers(0, c.max_nodes, most)) | {0, c.max_nodes - 1})
+
+
+CASES = [
+    # lens, counts, heads, extra
+    ([1024], [5], 8, dict(main_dtype="bf16")),
+    ([0], [1], 64, {}),
+    ([0, 1, 2], [3, 0, 1], 64, dict(shape="forest")),
+    ([127, 128, 129, 130, 131, 132], [2, 4, 1, 3, 2, 5], 16, {}),
+    ([3000, 517, 640], [1, 128, 77], 1, dict(shape="chain")),
+    ([2047], [64], 24, dict(shape="star")),
+    ([5000, 90, 1300], [7, 2, 12], 64, {}),
+    ([5000, 90, 1300], [7, 2, 12], 64, dict(win_dtype="fp8")),
+    ([2600, 700], [5, 9], 128, dict(main_dtype="bf16", win_dtype="fp8", shape="chain")),
+    ([70000, 300, 140], [3, 6, 2], 64, dict(ratio=128)),
+    ([40000, 33000], [9, 4], 10, dict(ratio=128, main_dtype="bf16")),
+    ([9000, 400, 100], [4, 6, 3], 64, dict(topk=300)),
+    ([9000, 2000], [3, 2], 64, dict(topk=512, shape="chain")),
+    ([3000, 150], [5, 2], 6, dict(topk=1)),
+    ([3000, 2500], [2, 3], 100, dict(topk=2048, main_dtype="bf16")),
+    ([1500, 800], [3, 40], 8, dict(window=300)),
+    ([1500, 800], [3, 40], 8, dict(window=40)),
+]
+
+
+@pytest.mark.parametrize("lens,counts,heads,extra", CASES)
+def test_attention_matches_the_oracle(lens, counts, heads, extra):
+    c = TreeCase(801 + heads + lens[0], lens, counts, heads, spare=3, **extra)
+    d = c.device()
+    c.run(d)
+    torch.cuda.synchronize()
+    assert int(d["st"].item()) == 0
+    c.check(d["out"], nodes=chosen(c, synth.rng(1)))
+    assert (d["out"][c.cu[-1]:] == 7.0).all()  # rows behind the last sequence
+
+
+@pytest.mark.parametrize("heads,extra", [(64, {}), (8, dict(main_dtype="bf16")), (64, dict(topk=100))])
+def test_attention_with_fp32_queries(heads, extra):
+    c = TreeCase(840, [1800, 333], [6, 3], heads, **extra)
+    d = c.device(q_fp32=True)
+    c.run(d)
+    c.check(d["out"], q_fp32=True)
+    assert int(d["st"].item()) == 0
+
+
+def test_a_path_equals_decode_after_appending_it():
+    """One chain per sequence: the last node's output against
+    v4kv_decode_attention with the chain's rows written into the window. Each
+    call is within its own bound of the same fp64 value; the decode's bound is
+    1e-2 of the largest output, the tree's is smaller."""
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(850, [1021, 600, 128], [3, 3, 3], 64, shape="chain")
+    d = c.device()
+    c.run(d)
+    win = c.win.to_cuda()
+    for b, L in enumerate(c.lens):
+        for i in range(3):
+            page = int(c.win.bt[b, (L + i) // 256])
+            assert page >= 0
+            win.data[page, (L + i) % 256] = d["k_tree"][c.cu[b] + i]
+    rows = [int(c.cu[b]) + 2 for b in range(3)]
+    lens = d["lens"] + 3
+    out = torch.empty(3, 64, 512, dtype=torch.bfloat16, device="cuda")
+    n = v4kv.v4kv_workspace_size(v4kv.V4KV_OP_DECODE, 3, 64, 1024, 4, W, 0, d["main"].dtype_code)
+    v4kv.v4kv_decode_attention(d["q"][rows].contiguous(), d["main"], win, lens, 1024, 4, W, out,
+                               torch.empty(n, dtype=torch.uint8, device="cuda"), dev_status=d["st"])
+    a, b = d["out"][rows].float(), out.float()
+    assert float((a - b).abs().max()) <= 2e-2 * float(b.abs().max())
+    assert int(d["st"].item()) == 0
+
+
+@pytest.mark.parametrize("main_dtype,win_dtype", [("fp8", "bf16"), ("fp8", "fp8"), ("bf16", "bf16")])
+def test_rows_that_are_not_attended_may_hold_anything(main_dtype, win_dtype):
+    """NaN and infinities in sibling nodes, in slots behind the visible entries,
+    before the window and behind the cached tokens change nothing."""
+    c = TreeCase(860, [1100, 523], [9, 6], 64, main_dtype=main_dtype, win_dtype=win_dtype)
+    clean, dirty = c.device(), c.device()
+    c.run(clean)
+    bad16 = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").to(torch.bfloat16)
+    for b, L in enumerate(c.lens):
+        vis = max(0, L + max(c.counts) - W) // 4
+        for j in range(vis, -(-L // 4)):
+            page = int(c.main.bt[b, j // 64])
+            if main_dtype == "fp8":
+                dirty["main"].data[page, j % 64] = 0x7F if j % 2 else 0xFF
+                dirty["main"].scales[page, j % 64] = float("nan") if j % 3 else float("inf")
+            else:
+                dirty["main"].data[page, j % 64] = bad16[j % 3]
+        for t in list(range(max(0, L - W) // 256 * 256, max(0, L + 1 - W))) + list(range(L, -(-L // 256) * 256)):
+            page = int(c.win.bt[b, t // 256])
+            if win_dtype == "fp8":
+                dirty["win"].data[page, t % 256] = 0x7F
+                dirty["win"].scales[page, t % 256] = float("nan")
+            else:
+                dirty["win"].data[page, t % 256] = bad16[t % 3]
+    c.run(dirty)
+    assert torch.equal(clean["out"], dirty["out"])
+    # a node's row reaches its own descendants only
+    hit = 3
+    dirty["k_tree"][int(c.cu[0]) + hit] = bad16[0]
+    dirty["k_tree"][int(c.cu[1]) + hit, 17] = float("inf")
+    c.run(dirty)
+    for b in range(2):
+        for i in range(c.counts[b]):
+            row = int(c.cu[b]) + i
+            if hit in tree.family(c.parents[c.cu[b]:c.cu[b + 1]], i):
+                # the formula gives NaN at the dims that hold it; elsewhere too where the score is not -inf
+                assert torch.isnan(dirty["out"][row] if b == 0 else dirty["out"][row, :, 17]).all()
+            else:
+                assert torch.equal(dirty["out"][row], clean["out"][row])
+
+
+def test_entries_visible_to_the_deeper_nodes_only():
+    """Entries that only the deeper nodes of a chain see hold NaN codes."""
+    c = TreeCase(861, [1027], [14], 64, shape="chain")
+    d = c.device()
+    c.run(d)
+    clean = d["out"].clone()
+    L = 1027
+    j = (L + 1 - W) // 4 + 1  # visible from depth 4 * (j + 1) - (L + 1 - W) on
+    first = 4 * (j + 1) - (L + 1 - W)
+    assert 0 < first < 13
+    d["main"].data[int(c.main.bt[0, j // 64]), j % 64, 5] = 0x7F
+    c.run(d)
+    assert torch.equal(d["out"][:first], clean[:first])
+    assert torch.isnan(d["out"][first:]).all()
+
+
+def test_scales_of_any_value():
+    c = TreeCase(862, [1500], [4], 64)
+    r = synth.rng(9)
+    c.main.scales[:] *= np.exp2(r.integers(-12, 4, c.main.scales.shape)).astype(np.float32)
+    c.main.scales[r.random(c.main.scales.shape) < 0.1] = 0.0
+    c.main.scales[r.random(c.main.scales.shape) < 0.2] *= -1.0
+    d = c.device()
+    c.run(d)
+    c.check(d["out"])
+
+
+def test_scores_that_grow_along_the_context():
+    """A query along one direction whose entries' magnitude grows: the running
+    maximum rises again and again, by far more than any fixed range."""
+    c = TreeCase(863, [3000], [3], 64)
+    direction = np.sign(c.q[:, :1].mean(axis=(0, 1)))[None, None]
+    c.q = codecs.bf16_round(np.broadcast_to(direction, c.q.shape) * (1 + 0.01 * c.q))
+    flat = codecs.e4m3_decode(c.main.data) * c.main.scales[..., None]
+    for j in range(-(-3000 // 4)):
+        page = int(c.main.bt[0, j // 64])
+        flat[page, j % 64] = 0.02 * flat[page, j % 64] + direction[0, 0] * 0.01 * j
+    codes, scales = codecs.quantize_entry(flat.reshape(-1, 512).astype(np.float32))
+    c.main.data[:] = codes.reshape(c.main.data.shape)
+    c.main.scales[:] = scales.reshape(c.main.scales.shape)
+    d = c.device()
+    c.run(d)
+    out = d["out"].float().cpu().numpy()
+    for i in range(3):
+        ref, mass = c.oracle(0, i)
+        # scores reach 170 here: their fp32 sums are off by up to 512 * 170 * 2^-24
+        tol = (2.0 ** -9 + 2 * 512 * 170 * 2.0 ** -24) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max()
+        assert (np.abs(out[i] - ref) <= tol).all()
+
+
+def test_bad_inputs_are_flagged_and_skipped():
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(870, [900, 700], [5, 4], 64)
+    d = c.device()
+    c.run(d)
+    clean = d["out"].clone()
+    # a parent behind its child: the child is a root
+    d["parents"][2] = 2
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_INDEX
+    keep = c.parents.copy()
+    c.parents[2] = -1
+    c.check(d["out"])
+    c.parents = keep
+    # a page outside the pool: its entries are left out
+    d = c.device()
+    d["main"].block_table[1, 0] = 10 ** 6
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_PAGE
+    assert torch.equal(d["out"][:5], clean[:5])
+    # a length above the host's bound is clamped, a sequence with too many nodes cut
+    d = c.device()
+    d["lens"][0] = 10 ** 6
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_OVERFLOW
+    assert torch.equal(d["out"][:5], clean[:5])
+    d = c.device()
+    c.max_nodes = 4
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_OVERFLOW
+    assert torch.equal(d["out"][:4], clean[:4]) and (d["out"][4] == 7.0).all()
+    assert torch.equal(d["out"][5:9], clean[5:9])
+    c.max_nodes = 5
+    # offsets outside the arrays reach nothing
+    d = c.device()
+    d["cu"].copy_(torch.tensor([0, 5, 10 ** 6], dtype=torch.int32))
+    c.run(d)
+    assert int(d["st"].item()) & v4kv.V4KV_DEV_OVERFLOW
+    assert torch.equal(d["out"], clean)
+    # a top-k entry the sequence does not hold
+    c = TreeCase(871, [900], [3], 64, topk=50)
+    d = c.device()
+    c.run(d)
+    clean = d["out"].clone()
+    c.topk[1, 7] = -1
+    d["topk"] = torch.from_numpy(c.topk).cuda()
+    d["topk"][1, 7] = 225
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_INDEX
+    c.check(d["out"])
+
+
+def test_host_refusals_that_need_a_device():
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(872, [300], [2], 64)
+    d = c.device()
+    small = dict(d, ws=d["ws"][:128])
+    with pytest.raises(v4kv.V4KVError) as e:
+        c.run(small)
+    assert e.value.status == v4kv.V4KV_ERR_INVALID_ARG
+    off = torch.empty(d["ws"].numel() + 16, dtype=torch.uint8, device="cuda")[16:]
+    with pytest.raises(v4kv.V4KVError):
+        c.run(dict(d, ws=off))
+    assert (d["out"] == 7.0).all()
+
+
+def test_no_nodes_at_all():
+    c = TreeCase(873, [300, 20], [0, 0], 64)
+    d = c.device()
+    c.run(d)
+    assert int(d["st"].item()) == 0
+
+
+def test_streams_graphs_and_repeats_give_the_same_bits():
+    c = TreeCase(880, [9000, 700, 33], [6, 1, 11], 64)
+    e = TreeCase(881, [20000, 4000], [3, 8], 16, ratio=128)
+    d, f = c.device(), e.device()
+    c.run(d)
+    e.run(f)
+    ref, ref2 = d["out"].clone(), f["out"].clone()
+    # two calls at once, each with its own workspace
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        d["out"].fill_(0)
+        f["out"].fill_(0)
+        torch.cuda.synchronize()
+        c.run(d, stream=s1)
+        e.run(f, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(d["out"], ref) and torch.equal(f["out"], ref2)
+    # captured, then replayed with other lengths, nodes and values in the same buffers
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(d)
+        e.run(f)
+    other = TreeCase(882, [8500, 200, 40], [4, 7, 7], 64)
+    o = other.device()
+    other.max_len, other.max_nodes = c.max_len, c.max_nodes
+    o["ws"] = other.workspace(o)
+    other.run(o)
+    for name in ("q", "k_tree", "cu", "parents", "lens"):
+        d[name].copy_(o[name])
+    for p in ("main", "win"):
+        n = min(d[p].data.shape[0], o[p].data.shape[0])
+        d[p].data[:n].copy_(o[p].data[:n])
+        if d[p].scales is not None:
+            d[p].scales[:n].copy_(o[p].scales[:n])
+        table = torch.full_like(d[p].block_table, -1)
+        m = min(table.shape[1], o[p].block_table.shape[1])
+        table[:, :m] = o[p].block_table[:, :m]
+        assert int(table.max()) < n
+        d[p].block_table.copy_(table)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(d["out"], o["out"]) and torch.equal(f["out"], ref2)
+    assert int(d["st"].item()) == 0
+
+
+# ------------------------------------------------------------------ verification
+
+class VerifyCase:
+    def __init__(self, seed, counts, vocab, shape="tree", draft=True, dtype=torch.float32, spread=2.0, pad=0):
+        r = synth.rng(seed)
+        self.counts, self.vocab, self.shape = list(counts), vocab, shape
+        self.cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        n = self.N = int(self.cu[-1])
+        self.parents = np.concatenate([make_parents(r, k, shape) for k in counts] + [[]]).astype(np.int32)
+        x = synth.normal(r, (n, vocab), spread)
+        y = x + synth.normal(r, (n, vocab), 0.7)
+
+        def soft(v):
+            e = np.exp(v - v.max(axis=1, keepdims=True))
+            return torch.from_numpy((e / e.sum(axis=1, keepdims=True)).astype(np.float32)).to(dtype)
+
+        self.target, self.draft = soft(x), soft(y) if draft else None
+        q = soft(y).double().numpy()
+        self.tokens = np.zeros(n, dtype=np.int32)
+        for b, k in enumerate(counts):
+            for i in range(1, k):
+                row = q[self.cu[b] + self.parents[self.cu[b] + i]]
+                self.tokens[self.cu[b] + i] = min(vocab - 1, int(np.searchsorted(np.cumsum(row), r.random() * row.sum())))
+        self.u = r.random(n).astype(np.float32)
+        self.s = r.random(len(counts)).astype(np.float32)
+        self.pad, self.max_nodes = pad, max(max(counts), 1)
+
+    def run(self):
+        from paged_compressed_kv_b200 import v4kv
+
+        def rows(t):
+            wide = torch.full((self.N, self.vocab + self.pad), float("nan"), dtype=t.dtype, device="cuda")
+            wide[:, :self.vocab] = t.cuda()
+            return wide[:, :self.vocab]
+
+        i32 = dict(dtype=torch.int32, device="cuda")
+        B = len(self.counts)
+        path, n, nxt = torch.full((B, self.max_nodes), 99, **i32), torch.full((B,), 99, **i32), torch.full((B,), 99, **i32)
+        st = torch.zeros(1, **i32)
+        v4kv.v4kv_tree_verify(rows(self.target), torch.from_numpy(self.cu).cuda(), torch.from_numpy(self.parents).cuda(),
+                              torch.from_numpy(self.tokens).cuda(), torch.from_numpy(self.u).cuda(),
+                              torch.from_numpy(self.s).cuda(), self.max_nodes, path, n, nxt,
+                              draft=rows(self.draft) if self.draft is not None else None, dev_status=st)
+        return path.cpu().numpy(), n.cpu().numpy(), nxt.cpu().numpy(), int(st.item())
+
+    def check(self):
+        path, n, nxt, st = self.run()
+        assert st == 0
+        t = self.target.double().numpy()
+        q = self.draft.double().numpy() if self.draft is not None else None
+        for b, k in enumerate(self.counts):
+            lo, hi = self.cu[b], self.cu[b + 1]
+            if k == 0:
+                assert n[b] == 0 and nxt[b] == -1 and (path[b] == -1).all()
+                continue
+            want, token = tree.verify(t[lo:hi], None if q is None else q[lo:hi], self.parents[lo:hi],
+                                      self.tokens[lo:hi], self.u[lo:hi], self.s[b])
+            assert list(path[b]) == want + [-1] * (self.max_nodes - len(want)), b
+            assert n[b] == len(want) and nxt[b] == token, (b, nxt[b], token)
+        return n
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 3, 31, 1000, 4099, 50257])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_matches_the_oracle(vocab, draft):
+    n = VerifyCase(900 + vocab, [4, 1, 0, 9, 6, 6, 13, 6], vocab, draft=draft).check()
+    if vocab == 1000 and draft:
+        assert n.max() > 1  # paths of more than the root are among them
+
+
+@pytest.mark.parametrize("shape,pad,dtype", [("chain", 0, torch.float32), ("star", 3, torch.float32),
+                                             ("tree", 1, torch.bfloat16), ("star", 0, torch.bfloat16)])
+def test_verify_shapes_strides_and_types(shape, pad, dtype):
+    VerifyCase(930 + pad, [7, 30, 128, 3, 5], 517, shape=shape, pad=pad, dtype=dtype).check()
+    VerifyCase(931 + pad, [7, 30, 128, 3, 5], 518, shape=shape, pad=pad, dtype=dtype, draft=False).check()
+
+
+def test_verify_edges():
+    from paged_compressed_kv_b200 import v4kv
+    # equal draft and target: every child that is first asked is accepted
+    c = VerifyCase(940, [6, 6, 6], 300, shape="chain")
+    c.draft = c.target.clone()
+    assert (c.check() == 6).all()
+    # one-hot targets: the guess is taken exactly when it is the token
+    c = VerifyCase(941, [4, 4], 64, shape="chain", draft=False)
+    c.target = torch.zeros_like(c.target)
+    c.target[torch.arange(8), torch.arange(8) + 3] = 1.0
+    c.tokens = np.array([0, 3, 4, 60, 0, 7, 60, 9], dtype=np.int32)
+    assert list(c.check()) == [3, 2]
+    # numbers at the ends of the unit interval; duplicate children
+    c = VerifyCase(942, [5, 5, 5], 40, shape="star", draft=False)
+    c.tokens[:] = 11
+    c.u[:], c.s[:] = 1.0 - 2.0 ** -24, [0.0, 1.0 - 2.0 ** -24, 1.0]
+    c.check()
+    c = VerifyCase(943, [5, 5, 5], 40, shape="star")
+    c.u[:], c.s[:] = 1.0 - 2.0 ** -24, [0.0, 1.0 - 2.0 ** -24, 1.0]
+    c.check()
+    # a token outside the vocabulary, a row without mass, a second root
+    c = VerifyCase(944, [3, 3], 40, shape="chain")
+    c.tokens[1], c.tokens[5] = 40, -1
+    path, n, nxt, st = c.run()
+    assert st == v4kv.V4KV_DEV_BAD_INDEX and n[0] == 1
+    c = VerifyCase(945, [2, 2], 40, shape="chain", draft=False)
+    c.target[0] = 0.0
+    path, n, nxt, st = c.run()
+    assert st == v4kv.V4KV_DEV_BAD_PROB and nxt[0] == -1 and n[0] == 1 and nxt[1] >= 0
+    c = VerifyCase(946, [3], 40, shape="forest")
+    assert list(c.check()) == [1]
+
+
+# ------------------------------------------------------------------ packing and a whole step
+
+@pytest.mark.parametrize("dim,per_channel", [(8, False), (512, False), (512, True), (1024, True), (200, True)])
+def test_gather_packs_the_accepted_rows(dim, per_channel):
+    from paged_compressed_kv_b200 import v4kv
+    r = synth.rng(950 + dim)
+    counts = [5, 0, 1, 30, 2, 128] + [3] * 300
+    cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    N, B, most = int(cu[-1]), len(counts), max(counts)
+    path, n = np.full((B, most), -1, dtype=np.int32), np.zeros(B, dtype=np.int32)
+    for b, k in enumerate(counts):
+        n[b] = r.integers(1, k + 1) if k else 0
+        path[b, :n[b]] = np.sort(r.permutation(k)[:n[b]])
+    x = synth.bf16_tensor(synth.normal(r, (N, dim))).cuda()
+    gate = torch.from_numpy(synth.normal(r, (N, dim) if per_channel else N)).cuda()
+    total = int(n.sum())
+    rows = torch.from_numpy(np.concatenate([cu[b] + path[b, :n[b]] for b in range(B)])).long().cuda()
+    for cap in (N, total, total - 7):
+        xo = torch.full((cap, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+        go = torch.full((cap, dim) if per_channel else (cap,), 3.0, device="cuda")
+        cuo = torch.full((B + 1,), -5, dtype=torch.int32, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        v4kv.v4kv_tree_gather(x, gate, torch.from_numpy(cu).cuda(), torch.from_numpy(path).cuda(),
+                              torch.from_numpy(n).cuda(), xo, go, cuo, dev_status=st)
+        m = min(cap, total)
+        assert torch.equal(xo[:m], x[rows[:m]]) and torch.equal(go[:m], gate[rows[:m]])
+        assert (xo[m:] == 3.0).all() and (go[m:] == 3.0).all()
+        want = np.minimum(np.concatenate([[0], np.cumsum(n)]), cap)
+        assert (cuo.cpu().numpy() == want).all()
+        assert int(st.item()) == (v4kv.V4KV_DEV_OVERFLOW if cap < total else 0)
+    path[3, 0] = 30
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    xo = torch.full((N, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+    go = torch.full((N, dim) if per_channel else (N,), 3.0, device="cuda")
+    v4kv.v4kv_tree_gather(x, gate, torch.from_numpy(cu).cuda(), torch.from_numpy(path).cuda(),
+                          torch.from_numpy(n).cuda(), xo, go, cuo, dev_status=st)
+    assert int(st.item()) == v4kv.V4KV_DEV_BAD_INDEX
+    at = int(n[:3].sum())
+    assert not xo[at].any() and not go[at].any() and torch.equal(xo[at + 1:total], x[rows[at + 1:]])
+
+
+def test_a_speculative_step_equals_appending_the_accepted_tokens():
+    """The operators together, as a serving loop runs them and without reading
+    anything back: rotate q and K of the drafted nodes, attend, verify, pack,
+    append. The cache afterwards is bit for bit the one that appending the
+    accepted tokens gives, and the next step's attention agrees with it."""
+    from paged_compressed_kv_b200 import PagedPool, Rope, v4kv
+    r = synth.rng(960)
+    B, H, ratio, T, vocab = 3, 8, 4, 6, 97
+    lens = [517, 130, 255]
+    dev = dict(device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def pools():
+        main = PagedPool(data=torch.zeros(3 * B, 64, 512, dtype=torch.uint8, **dev),
+                         scales=torch.zeros(3 * B, 64, **dev),
+                         block_table=torch.arange(3 * B, **i32).view(B, 3).flip(1).contiguous())
+        win = PagedPool(data=torch.zeros(3 * B, 256, 512, dtype=torch.bfloat16, **dev),
+                        block_table=torch.arange(3 * B, **i32).view(3, B).t().contiguous())
+        state = (torch.zeros(B, ratio, 512, dtype=torch.bfloat16, **dev), torch.zeros(B, ratio, **dev))
+        return main, win, state
+
+    bias = torch.from_numpy(synth.normal(r, ratio, 0.5)).cuda()
+    prompt = synth.bf16_tensor(synth.normal(r, (sum(lens), 512))).cuda()
+    pgate = torch.from_numpy(synth.normal(r, sum(lens))).cuda()
+    parents = torch.tensor(make_parents(r, T, "tree") * B, **i32)
+    cu = torch.arange(B + 1, **i32) * T
+    x = synth.bf16_tensor(synth.normal(r, (B * T, 512))).cuda()
+    gate = torch.from_numpy(synth.normal(r, B * T)).cuda()
+    q = torch.from_numpy(synth.normal(r, (B * T, H, 512))).cuda()
+    depth = torch.tensor([len(tree.family(parents[:T].tolist(), i)) - 1 for i in range(T)] * B, **i32)
+    target = torch.softmax(torch.from_numpy(synth.normal(r, (B * T, vocab), 3.0)).cuda(), -1)
+    tokens = target.argmax(-1).to(torch.int32).view(B, T).gather(1, parents.view(B, T).clamp(min=0).long()).view(-1).contiguous()
+    u, s = torch.from_numpy(r.random(B * T).astype(np.float32)).cuda() * 0.5, torch.from_numpy(r.random(B).astype(np.float32)).cuda()
+    st = torch.zeros(1, **i32)
+
+    def append(main, win, state, x, gate, cu_seq, start):
+        v4kv.v4kv_compress_append(x, gate, cu_seq, start, bias, ratio, state[0], state[1], main, None, None, window=win,
+                                  window_len=W, rope=Rope(), dev_status=st)
+
+    def attend(main, win, L, nodes_q, cu_n, par, k_rows, n):
+        out = torch.empty(nodes_q.shape, dtype=torch.bfloat16, **dev)
+        size = v4kv.v4kv_tree_workspace_size(B, H, nodes_q.shape[0], n, 700, ratio, W, 0, main.dtype_code)
+        v4kv.v4kv_tree_attention(nodes_q, cu_n, par, k_rows, main, win, L, n, 700, ratio, W, out,
+                                 torch.empty(max(size, 256), dtype=torch.uint8, **dev), dev_status=st)
+        return out
+
+    def rotate(v, pos):
+        out = torch.empty(v.shape, dtype=torch.bfloat16, **dev)
+        v4kv.v4kv_qk_prepare(v.contiguous(), pos, out, rope=Rope())
+        return out
+
+    start = torch.tensor(lens, **i32)
+    zero = torch.zeros(B, **i32)
+    cu_p = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), **i32)
+    main, win, state = pools()
+    append(main, win, state, prompt, pgate, cu_p, zero)
+    pos = start.repeat_interleave(T) + depth
+    out = attend(main, win, start, rotate(q, pos), cu, parents, rotate(x.float().view(-1, 1, 512), pos).view(-1, 512), T)
+    path, n_path, nxt = torch.empty(B, T, **i32), torch.empty(B, **i32), torch.empty(B, **i32)
+    v4kv.v4kv_tree_verify(target, cu, parents, tokens, u, s, T, path, n_path, nxt, dev_status=st)
+    xo, go, cuo = torch.zeros_like(x), torch.zeros_like(gate), torch.empty(B + 1, **i32)
+    v4kv.v4kv_tree_gather(x, gate, cu, path, n_path, xo, go, cuo, dev_status=st)
+    append(main, win, state, xo, go, cuo, start)   # all of xo's rows, as the host does not know the count
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.isfinite(out.float()).all()
+    n = n_path.tolist()
+    assert max(n) > 1, n  # something was accepted
+    # the same tokens appended directly
+    main2, win2, state2 = pools()
+    append(main2, win2, state2, prompt, pgate, cu_p, zero)
+    rows = torch.cat([cu[b] + path[b, :n[b]] for b in range(B)]).long()
+    append(main2, win2, state2, x[rows].contiguous(), gate[rows].contiguous(),
+           torch.tensor(np.concatenate([[0], np.cumsum(n)]), **i32), start)
+    assert torch.equal(main.data, main2.data) and torch.equal(main.scales, main2.scales)
+    assert torch.equal(win.data, win2.data)
+    # an accepted path's last node equals a root attending the appended cache one token earlier:
+    # the same items, in the window instead of the tree
+    last = torch.stack([cu[b] + path[b, n[b] - 1] for b in range(B)]).long()
+    one = attend(main, win, start + n_path - 1, rotate(q, pos)[last].contiguous(), torch.arange(B + 1, **i32),
+                 torch.full((B,), -1, **i32), rotate(x.float().view(-1, 1, 512), pos).view(-1, 512)[last].contiguous(), 1)
+    a, b = out[last].float(), one.float()
+    assert float((a - b).abs().max()) <= 2e-2 * float(b.abs().max())
+    assert int(st.item()) == 0
