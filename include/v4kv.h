@@ -400,7 +400,7 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  * Numerics: every operand of the tensor cores is one or two fp8-e4m3 terms.
  * Cached codes are exact. A bf16 row (an entry, a window token, k_tree or q) is
  * split into two terms relative to its largest magnitude A, exact for values
- * of at least 2^-13 A and within 2^-22 A below; an fp32 q is
+ * of at least 2^-13 A and within 2^-21 A below; an fp32 q is
  * rounded to such terms (relative 2^-9). Softmax weights are rounded to two
  * terms (relative 2^-9) with a power-of-two scale per 32 items; accumulation,
  * maxima and sums are fp32. Any fp8 scale is valid, zero and negative ones too.
