@@ -240,5 +240,8 @@ v4kv_status decode_check_args(const void* q, int32_t q_dtype, int32_t batch, int
 // swizzle), boxes of `row_bytes` x `box_rows`. base must be 16-byte aligned.
 cudaError_t encode_rows_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t row_bytes,
                            uint32_t box_rows);
+// The same with boxes of `box_bytes` (at most 128) of each row.
+cudaError_t encode_cols_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t row_bytes,
+                           uint32_t box_bytes, uint32_t box_rows);
 
 }  // namespace v4kv

@@ -30,8 +30,9 @@
 // The normaliser and the running reference are fp32. With block scales P needs
 // no fixed range, so the reference moves only when a score passes it by 2^40.
 //
-// Warps: 0-7 softmax (thread = item of the tile and 32 of the rows; also the
-// unit's Q and its epilogue), 8-11 load tiles, 12 issues the MMAs.
+// Warps: 0-7 softmax (a thread has 4 items of the tile and 8 of the rows; also
+// the unit's Q and its epilogue), 8-11 load tiles, 12 issues the MMAs, 13 and
+// 14 resolve the even and odd tiles' row addresses ahead.
 //
 // Schedule: the tiles of all units are one list; the prep kernel gives each
 // block of the grid (one per SM) an equal share by estimated cost. A block that
@@ -48,7 +49,8 @@ namespace {
 constexpr int kR = 64;    // rows of a unit
 constexpr int kT = 128;   // items of a tile
 constexpr int kD = 512;
-constexpr int kThreads = 416;
+constexpr int kThreads = 480;
+constexpr int kRing = 4;  // tiles whose rows are resolved ahead
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr float kRaise = 40.f;   // log2 by which a score may pass its reference
 constexpr int kPairs = kRopeTable;
@@ -59,15 +61,16 @@ constexpr uint32_t kVOff = 65536;             // 2 stages of 4 x [128 items x 12
 constexpr uint32_t kStage = 65536;
 constexpr uint32_t kChunk = 16384;
 constexpr uint32_t kPOff = 196608;            // [128 items x (64 hi, 64 lo)]
-constexpr uint32_t kMetaOff = 212992;         // [2][128] {scale, 0 or -inf}
-constexpr uint32_t kRowOff = kMetaOff + 2048; // [64] {score factor, reference}
+constexpr uint32_t kMetaOff = 212992;         // [kRing][128] {scale, 0 or -inf}
+constexpr uint32_t kPtrOff = kMetaOff + kRing * 1024;  // [kRing][128] row addresses, bit 0: fp8
+constexpr uint32_t kRowOff = kPtrOff + kRing * 1024; // [64] {score factor, reference}
 constexpr uint32_t kAncOff = kRowOff + 512;   // [64] ancestors of the row's node, 128 bits
-constexpr uint32_t kVisOff = kAncOff + 1024;  // [64] {visible entries, first visible token}
-constexpr uint32_t kRedOff = kVisOff + 512;   // [8][32] reductions over a warp's items
+constexpr uint32_t kVisOff = kAncOff + 1024;  // [64] {visible entries, first visible token, node}
+constexpr uint32_t kRedOff = kVisOff + 1024;   // [8][32] reductions over a warp's items
 constexpr uint32_t kSfOff = kRedOff + 1024;   // [64] block scales of P, a byte per 32 items
 constexpr uint32_t kFacOff = kSfOff + 256;    // [64] per-row factors
 constexpr uint32_t kBarOff = kFacOff + 256;
-constexpr uint32_t kMiscOff = kBarOff + 128;
+constexpr uint32_t kMiscOff = kBarOff + 192;
 constexpr uint32_t kSmemBytes = kMiscOff + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
@@ -83,8 +86,10 @@ constexpr uint32_t kCols = 512;
 
 struct Bars {
   uint64_t kv_full[2], kv_empty[2];
-  uint64_t q_full, s_full, p_full, pv_done, drain;
+  uint64_t addr_full[kRing], addr_free[kRing];
+  uint64_t q_full, s_full, p_full, pv_done, epi, drain;
 };
+static_assert(sizeof(Bars) <= 192, "barrier area");
 
 // What the prep kernel leaves in the workspace.
 struct TreeWs {
@@ -104,6 +109,8 @@ struct Params {
   int grid;
   int hc;        // units per node (per_node)
   int per_node;  // a unit's rows belong to one node
+  int pages;     // tiles of entries are whole pages of 64 rows, loaded by TMA
+  CUtensorMap map;  // boxes of 64 rows x 128 bytes of main_cache
 };
 
 __device__ __forceinline__ int seq_len(const TreeArgs& a, int b) {
@@ -307,77 +314,96 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
-// maximum or sum of 32 per-lane values over a warp's lanes: lane l ends with
-// the result of value l (31 shuffles)
-template <bool kMax>
-__device__ __forceinline__ float reduce_scatter32(float* v, int lane) {
-#pragma unroll
-  for (int n = 16; n > 0; n >>= 1) {
-    const bool upper = (lane & n) != 0;
-#pragma unroll
-    for (int k = 0; k < n; ++k) {
-      const float mine = upper ? v[n + k] : v[k], other = upper ? v[k] : v[n + k];
-      const float x = __shfl_xor_sync(0xffffffffu, other, n);
-      v[k] = kMax ? fmaxf(mine, x) : mine + x;
-    }
-  }
-  return v[0];
-}
-
 // ------------------------------------------------------------------ loading (warps 8-11)
 
-// where an item's row is: null for an item that has none
-struct Item {
-  const uint8_t* p;
-  float scale;
-  bool fp8;
-};
-
-__device__ __forceinline__ Item item_of(const Params& p, const Unit& x, const Tile& t, int r, int32_t* st) {
+// Lane l resolves items l, l + 32, l + 64, l + 96 of a tile: their rows'
+// addresses (bit 0: fp8 codes; 0: no such item) and scales. The loads go in
+// phases (top-k entry, block table, scale), the four of a phase independent of
+// one another.
+__device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, const Tile& t, int lane,
+                                             unsigned long long* rows, float2* meta) {
   const TreeArgs& a = p.a;
-  Item it{nullptr, 0.f, false};
-  if (r >= t.count) return it;
-  int j = t.first + r;
-  const PoolArgs* pool;
-  if (t.entries) {
-    pool = &a.main;
-    if (a.topk) {
-      j = a.topk[(size_t)(x.q.s.first + x.node0) * a.k + j];
-      if (j < 0) return it;
-      if (j >= (x.q.L + a.ratio - 1) / a.ratio) {
-        flag(st, V4KV_DEV_BAD_INDEX);
-        return it;
-      }
-    }
-  } else if (j < x.n_win) {
-    pool = &a.window;
-    j += x.w0;
-  } else {
-    j -= x.n_win;
-    if (p.per_node) {  // the j-th of the node's ancestors
-      const uint4 m4 = p.w.anc[x.q.s.first + x.node0];
-      const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
-      int k = 0;
-      while (k < 3 && j >= __popc(m[k])) j -= __popc(m[k++]);
-      j = 32 * k + (int)__fns(m[k], 0, j + 1);
-    }
-    it.p = reinterpret_cast<const uint8_t*>(a.k_tree + (size_t)(x.q.s.first + j) * kD);
-    it.scale = 1.f;
-    return it;
+  int j[4], pg[4], err = 0;
+  bool tree[4];
+  const bool main = t.entries;
+  const PoolArgs& pool = main ? a.main : a.window;
+  const int32_t* bt = pool.block_table + (size_t)x.b * pool.max_blocks;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int k = lane + 32 * r;
+    j[r] = k < t.count ? t.first + k : -1;
+    tree[r] = !main && j[r] >= x.n_win;
+    if (main && a.topk && j[r] >= 0) j[r] = a.topk[(size_t)(x.q.s.first + x.node0) * a.k + j[r]];
   }
-  const int pg = page_of(pool->block_table + (size_t)x.b * pool->max_blocks, pool->max_blocks, j, pool->spb,
-                         pool->num_pages, st);
-  if (pg < 0) return it;
-  const size_t slot = (size_t)pg * pool->spb + j % pool->spb;
-  it.fp8 = pool->dtype == V4KV_FP8_E4M3;
-  it.scale = it.fp8 ? pool->scales[slot] : 1.f;
-  if (!isfinite(it.scale)) it.scale = __int_as_float(0x7fffffff);
-  it.p = static_cast<const uint8_t*>(pool->data) + slot * (it.fp8 ? kD : 2 * kD);
-  return it;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    pg[r] = -1;
+    if (tree[r] || j[r] < 0) continue;
+    if (main && a.topk && j[r] >= (x.q.L + a.ratio - 1) / a.ratio) {
+      err |= V4KV_DEV_BAD_INDEX;
+      j[r] = -1;
+      continue;
+    }
+    if (!main) j[r] += x.w0;
+    if (j[r] / pool.spb >= pool.max_blocks) {
+      err |= V4KV_DEV_BAD_SLOT;
+      j[r] = -1;
+      continue;
+    }
+    pg[r] = bt[j[r] / pool.spb];
+  }
+  const bool fp8 = pool.dtype == V4KV_FP8_E4M3;
+  float scale[4];
+  unsigned long long at[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    scale[r] = 1.f;
+    at[r] = 0;
+    if (j[r] < 0) continue;
+    if (tree[r]) {
+      int n = j[r] - x.n_win;
+      if (p.per_node) {  // the n-th of the node's ancestors
+        const uint4 m4 = p.w.anc[x.q.s.first + x.node0];
+        uint32_t m = m4.x;
+        int base = 0;
+        if (n >= __popc(m)) { n -= __popc(m); m = m4.y; base = 32; }
+        if (base == 32 && n >= __popc(m)) { n -= __popc(m); m = m4.z; base = 64; }
+        if (base == 64 && n >= __popc(m)) { n -= __popc(m); m = m4.w; base = 96; }
+        for (; n > 0; --n) m &= m - 1;
+        n = base + __ffs(m) - 1;
+      }
+      at[r] = reinterpret_cast<unsigned long long>(a.k_tree + (size_t)(x.q.s.first + n) * kD);
+    } else if (pg[r] < 0 || pg[r] >= pool.num_pages) {
+      err |= V4KV_DEV_BAD_PAGE;
+    } else {
+      const size_t slot = (size_t)pg[r] * pool.spb + j[r] % pool.spb;
+      if (fp8) scale[r] = pool.scales[slot];
+      at[r] = reinterpret_cast<unsigned long long>(pool.data) + slot * (fp8 ? kD : 2 * kD) + (fp8 ? 1 : 0);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    rows[lane + 32 * r] = at[r];
+    meta[lane + 32 * r] = at[r] ? make_float2(isfinite(scale[r]) ? scale[r] : __int_as_float(0x7fffffff), 0.f)
+                                : make_float2(0.f, -INFINITY);
+  }
+  if (err) flag(a.dev_status, err);
 }
 
 // Codes that some rows of the unit must not see may not be NaN (0 * NaN): such
@@ -390,36 +416,58 @@ __device__ __forceinline__ bool has_nan_code(uint4 c) {
   return bad;
 }
 
-// one row, the whole warp: lane takes dims 16 lane .. 16 lane + 15
-__device__ __forceinline__ void load_row(const Item& it, int r, int lane, uint8_t* hi_dst, uint8_t* lo_dst,
-                                         float2* meta) {
-  const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r, lane & 7);
-  uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-  float scale = it.scale;
-  if (it.p) {
-    bool bad;
-    if (it.fp8) {
-      hi = reinterpret_cast<const uint4*>(it.p)[lane];
+// largest magnitude of 16 bf16 values per lane over a warp, as fp32 bits
+__device__ __forceinline__ uint32_t amax_bf16(const uint4* r) {
+  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16;
+}
+
+// kN rows, the whole warp: lane takes dims 16 lane .. 16 lane + 15 of each;
+// all loads are in flight together
+template <int kN>
+__device__ __forceinline__ void load_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
+                                          uint8_t* lo_dst, float2* meta) {
+  uint4 raw[kN][2];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const unsigned long long row = rows[k];
+    const uint4* p = reinterpret_cast<const uint4*>(row & ~1ull);
+    raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
+    if (row) {
+      raw[k][0] = p[row & 1 ? lane : 2 * lane];
+      if (!(row & 1)) raw[k][1] = p[2 * lane + 1];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const unsigned long long row = rows[k];
+    const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r0 + k, lane & 7);
+    uint4 hi = raw[k][0], lo = make_uint4(0, 0, 0, 0);
+    float scale = 0.f;
+    bool bad, set = false;
+    if (row & 1) {
       bad = __any_sync(0xffffffffu, has_nan_code(hi));
     } else {
-      float v[16];
-      bf16x16(reinterpret_cast<const uint4*>(it.p) + 2 * lane, v);
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-      m = __reduce_max_sync(0xffffffffu, m);
+      const uint32_t m = amax_bf16(raw[k]);
       bad = m >= 0x7f800000u;
+      float v[16];
+      bf16x16(raw[k], v);
       split16(v, scale_up(m), hi, lo);
       scale = scale_down(m);
+      set = row != 0;
     }
     if (bad) {
       hi = lo = make_uint4(0, 0, 0, 0);
       scale = __int_as_float(0x7fffffff);
+      set = true;
     }
+    if (set && lane == 0) meta[r0 + k].x = scale;
+    *reinterpret_cast<uint4*>(hi_dst + off) = hi;
+    if (lo_dst) *reinterpret_cast<uint4*>(lo_dst + off) = lo;
   }
-  *reinterpret_cast<uint4*>(hi_dst + off) = hi;
-  if (lo_dst) *reinterpret_cast<uint4*>(lo_dst + off) = lo;
-  if (lane == 0) meta[r] = make_float2(scale, it.p ? 0.f : -INFINITY);
 }
 
 // ------------------------------------------------------------------ the sweep
@@ -445,10 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       tc::mbar_init(&bars->kv_full[s], 128);
       tc::mbar_init(&bars->kv_empty[s], 1);
     }
+    for (int s = 0; s < kRing; ++s) {
+      tc::mbar_init(&bars->addr_full[s], 32);
+      tc::mbar_init(&bars->addr_free[s], 1);
+    }
     tc::mbar_init(&bars->q_full, 256);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->p_full, 256);
     tc::mbar_init(&bars->pv_done, 1);
+    tc::mbar_init(&bars->epi, 2);
     tc::mbar_init(&bars->drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -473,61 +526,92 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   x.q = plan_of(p, x.b, nullptr);
   unit_set(p, x);
 
-  if (warp >= 8 && warp < 12) {
-    // ======================= tiles into the stages. `im` counts images: image
-    // im lives in stage im % 2.
-    const int w = warp - 8;
-    int32_t* st = a.dev_status;
+  if (warp >= 13) {
+    // ======================= row addresses and scales, up to kRing tiles ahead.
+    // Tile number `done` of the block (tiles without items do not count) is in
+    // slot done % kRing.
+    uint32_t done = 0;
     bool ok = true;
-    uint32_t im = 0;
     for (int i = 0; i < n_tiles && ok; ++i) {
       const Tile t = tile_of(p, x);
       if (t.count > 0) {
-        const uint32_t s = im & 1;
+        if ((done & 1) == (uint32_t)(warp - 13)) {
+          const uint32_t s = done % kRing;
+          if (done >= kRing) ok = tc::mbar_wait(&bars->addr_free[s], ((done - kRing) / kRing) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          resolve_tile(p, x, t, lane, reinterpret_cast<unsigned long long*>(sm + kPtrOff) + s * kT, meta + s * kT);
+          tc::mbar_arrive(&bars->addr_full[s]);
+        }
+        ++done;
+      }
+      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      flag(a.dev_status, V4KV_DEV_TIMEOUT);
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ======================= tiles into the stages. `im` counts images: image
+    // im lives in stage im % 2.
+    const int w = warp - 8;
+    bool ok = true;
+    uint32_t im = 0, done = 0;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const Tile t = tile_of(p, x);
+      if (t.count > 0) {
+        const uint32_t s = im & 1, slot = done % kRing;
+        ok = tc::mbar_wait(&bars->addr_full[slot], (done / kRing) & 1, abort_flag);
         for (int k = 0; k < t.images; ++k)
           if (im + k >= 2) ok = ok && tc::mbar_wait(&bars->kv_empty[(im + k) & 1], ((im + k - 2) >> 1) & 1, abort_flag);
-        if (!ok) break;
-        const Item mine = item_of(p, x, t, 32 * w + lane, st);
-        float2* mt = meta + s * kT;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const unsigned long long* rows = reinterpret_cast<const unsigned long long*>(sm + kPtrOff) + slot * kT + 32 * w;
+        float2* mt = meta + slot * kT;
         uint8_t* dst = sm + kVOff + s * kStage;
         if (t.images == 1) {
+          if (p.pages && t.first + kT <= x.n_all) {
+            // two whole pages, every row of them visible: eight boxes
+            if (w == 0 && lane == 0) tc::mbar_arrive_expect_tx(&bars->kv_full[s], kStage);
+            if (w == 0) {
+              __syncwarp();
+              if (lane < 8) {
+                const unsigned long long row = rows[64 * (lane >> 2)];
+                // a page that is missing is read behind the pool's end: zeros
+                const int y = row ? (int)(((row & ~1ull) - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
+                                  : a.main.num_pages * a.main.spb;
+                tc::tma_load_2d(sbase + kVOff + s * kStage + (lane & 3) * kChunk + (lane >> 2) * (kChunk / 2), &p.map,
+                                128 * (lane & 3), y, &bars->kv_full[s]);
+              }
+            }
+            if (w > 0 || lane > 0) tc::mbar_arrive(&bars->kv_full[s]);
+            im += 1;
+            ++done;
+            if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+            continue;
+          }
           // rows from `safe` on are hidden from some of the unit's rows
           const int safe = max(0, min(32, x.n_all - t.first - 32 * w));
-          mt[32 * w + lane] = make_float2(mine.scale, mine.p ? 0.f : -INFINITY);
-          const uint8_t* any = static_cast<const uint8_t*>(a.main.data);
 #pragma unroll 8
           for (int r = 0; r < 32; ++r) {
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.p), r));
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[r] & ~1ull);
             if (r < safe || !src)
               cp_async16(sbase + kVOff + s * kStage + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7),
-                         src ? src + 16 * lane : any, src != nullptr);
+                         src ? src + 16 * lane : static_cast<const uint8_t*>(a.main.data), src != nullptr);
           }
-          __syncwarp();
-          for (int r = safe; r < 32; ++r) {
-            Item it;
-            it.p = reinterpret_cast<const uint8_t*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.p), r));
-            it.scale = __shfl_sync(0xffffffffu, mine.scale, r);
-            it.fp8 = true;
-            if (it.p) load_row(it, 32 * w + r, lane, dst, nullptr, mt);
-          }
+          for (int r = safe; r < 32; ++r)
+            if (rows[r]) load_rows<1>(rows + r, 32 * w + r, lane, dst, nullptr, mt);
           asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
           uint8_t* lo = sm + kVOff + (s ^ 1) * kStage;
-#pragma unroll 4
-          for (int r = 0; r < 32; ++r) {
-            Item it;
-            it.p = reinterpret_cast<const uint8_t*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.p), r));
-            it.scale = __shfl_sync(0xffffffffu, mine.scale, r);
-            it.fp8 = __shfl_sync(0xffffffffu, (int)mine.fp8, r) != 0;
-            load_row(it, 32 * w + r, lane, dst, lo, mt);
-          }
+#pragma unroll 1
+          for (int r = 0; r < 32; r += 8) load_rows<8>(rows + r, 32 * w + r, lane, dst, lo, mt);
         }
         tc::fence_proxy_async_smem();
         for (int k = 0; k < t.images; ++k) tc::mbar_arrive(&bars->kv_full[(im + k) & 1]);
         im += t.images;
+        ++done;
       }
       if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
     }
@@ -598,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
                 }
             tc::mma_commit(&bars->kv_empty[s]);
           }
+          tc::mma_commit(&bars->addr_free[done % kRing]);
         }
         __syncwarp();
         filled = 1;
@@ -623,16 +708,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     if (!tc::mbar_wait(&bars->drain, 0, &never) && leader) flag(a.dev_status, V4KV_DEV_TIMEOUT);
     __syncwarp();
   } else {
-    // ======================= softmax: thread = item 32 (warp % 4) + lane of the
-    // tile and rows 32 hh .. 32 hh + 31. The two halves never wait for each other.
-    const int hh = warp >> 2, w = warp & 3, item = 32 * w + lane;
+    // ======================= softmax: warp w of half hh has items 32 w .. 32 w +
+    // 31 and rows 32 hh .. 32 hh + 31; a thread items 32 w + lane / 4 + 8 j
+    // (j < 4) and rows 32 hh + 8 c + m (c = lane % 4, m < 8). That is how the
+    // 16x256b tensor-memory load deals out S when row 8 c + 2 k + e of a half
+    // sits in Q's row 8 k + 2 c + e. The eight rows' factors, references and
+    // sums fit in registers, and a row's maximum over the items takes three
+    // shuffles. The two halves meet only between units,
+    // at a barrier with a limit.
+    const int hh = warp >> 2, w = warp & 3, c4 = lane & 3;
     const int bar = 1 + hh;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     float* red = reinterpret_cast<float*>(sm + kRedOff) + 128 * hh;       // [4][32]
     float* fac = reinterpret_cast<float*>(sm + kFacOff) + 32 * hh;        // [32]
     uint8_t* sf = sm + kSfOff + 128 * hh;                                  // [32][4]
-    const uint4* anc = reinterpret_cast<const uint4*>(sm + kAncOff);
-    const int2* vis = reinterpret_cast<const int2*>(sm + kVisOff);
+    const uint4* anc = reinterpret_cast<const uint4*>(sm + kAncOff) + 32 * hh + 8 * c4;
+    const int4* vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh + 8 * c4;
+    float2* my_ar = row_ar + 32 * hh + 8 * c4;
     if (hh == 0) {
       const uint32_t one = 0x7f7f7f7fu, low = 0x7b7b7b7bu;
       tmem_st4(lanes + kOne, one, one, one, one);
@@ -644,197 +736,275 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     }
     bool ok = true, seg_open = true, any = false;
     int seg_tile0 = 0;
-    uint32_t im = 0, done = 0, seg = 0;
-    float l[32];
+    uint32_t done = 0, seg = 0;
+    float l[8], fa[8], ref[8];
     for (int i = 0; i < n_tiles; ++i) {
       if (seg_open) {
-        // the unit's Q (every product that reads the last one's has completed:
-        // its S was read), the rows' factors, references and masks
+        // the unit's Q, the rows' factors, references and masks. Every product
+        // that reads the last unit's Q has completed (its S was read), and both
+        // halves are done with its place.
+        if (seg > 0) {
+          ok = tc::mbar_wait(&bars->epi, (seg - 1) & 1, abort_flag);
+          if (named_or(bar, !ok)) {
+            ok = false;
+            break;
+          }
+        }
         seg_open = false;
         any = false;
         seg_tile0 = x.tile;
-#pragma unroll
-        for (int n = 0; n < 32; ++n) l[n] = 0.f;
-        for (int k = 0; k < 8; ++k) {
-          const int n = 32 * hh + 8 * w + k;
-          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-          uint32_t m = 0;
-          if (n < x.nrows) {
-            float v[16];
-            const size_t at = (size_t)(x.row0 + n) * kD + 16 * lane;
-            if (a.q_dtype == V4KV_FP32) {
-              const float4* q4 = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 f = q4[e];
-                v[4 * e] = f.x; v[4 * e + 1] = f.y; v[4 * e + 2] = f.z; v[4 * e + 3] = f.w;
-              }
-            } else {
-              bf16x16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at), v);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-            m = __reduce_max_sync(0xffffffffu, m);
-            split16(v, scale_up(m), hi, lo);
-          }
+        auto put_q = [&](int k, uint4 hi, uint4 lo, uint32_t m) {
+          const int n = 8 * w + k;                                    // row of the half
+          const int at = 32 * hh + 8 * (k >> 1) + 2 * w + (k & 1);    // row of Q
           uint8_t* dst = sm + kQOff + (lane >> 3) * kChunk;
-          *reinterpret_cast<uint4*>(dst + tc::sw128_off(n, lane & 7)) = hi;
-          *reinterpret_cast<uint4*>(dst + tc::sw128_off(kR + n, lane & 7)) = lo;
+          *reinterpret_cast<uint4*>(dst + tc::sw128_off(at, lane & 7)) = hi;
+          *reinterpret_cast<uint4*>(dst + tc::sw128_off(kR + at, lane & 7)) = lo;
           if (lane == 0)
-            row_ar[n] = make_float2(m >= 0x7f800000u ? __int_as_float(0x7fffffff)
-                                                     : scale_down(m) * (a.sm_scale * 1.4426950408889634f),
-                                    kNone);
+            row_ar[32 * hh + n] = make_float2(m >= 0x7f800000u ? __int_as_float(0x7fffffff)
+                                                               : scale_down(m) * (a.sm_scale * 1.4426950408889634f),
+                                              kNone);
+        };
+        const int n0 = 32 * hh + 8 * w;
+        const size_t q_at = (size_t)(x.row0 + n0) * kD + 16 * lane;
+        if (a.q_dtype == V4KV_FP32) {
+#pragma unroll 1
+          for (int k0 = 0; k0 < 8; k0 += 2) {
+            float4 f[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[k][e] = n0 + k0 + k < x.nrows
+                              ? reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + q_at + (size_t)(k0 + k) * kD)[e]
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float* v = reinterpret_cast<const float*>(f[k]);
+              uint32_t m = 0;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+              m = __reduce_max_sync(0xffffffffu, m);
+              uint4 hi, lo;
+              split16(v, scale_up(m), hi, lo);
+              put_q(k0 + k, hi, lo, m);
+            }
+          }
+        } else {
+          uint4 raw[8][2];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              raw[k][e] = n0 + k < x.nrows
+                              ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + (size_t)k * kD)[e]
+                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t m = amax_bf16(raw[k]);
+            float v[16];
+            bf16x16(raw[k], v);
+            uint4 hi, lo;
+            split16(v, scale_up(m), hi, lo);
+            put_q(k, hi, lo, m);
+          }
         }
-        if (!p.per_node && w == 0) {
+        if (w == 0) {
           const int n = 32 * hh + lane;
-          const int node = n < x.nrows ? (int)((x.row0 - (long long)x.q.s.first * a.heads + n) / a.heads) : x.node0;
-          const int d = p.w.depth[x.q.s.first + node];
-          reinterpret_cast<uint4*>(sm + kAncOff)[n] = p.w.anc[x.q.s.first + node];
-          const int w0 = max(0, x.q.L + d + 1 - a.window_len);
-          reinterpret_cast<int2*>(sm + kVisOff)[n] = make_int2(w0 / a.ratio, w0);
+          int node = x.node0;  // per_node: the only one
+          if (!p.per_node && n < x.nrows) node = (x.u * kR + n) / a.heads;
+          node += x.q.s.first;
+          const int w0 = max(0, x.q.L + p.w.depth[node] + 1 - a.window_len);
+          reinterpret_cast<uint4*>(sm + kAncOff)[n] = p.w.anc[node];
+          reinterpret_cast<int4*>(sm + kVisOff)[n] = make_int4(w0 / a.ratio, w0, node, 0);
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         tc::mbar_arrive(&bars->q_full);
         named_sync(bar);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          l[m] = 0.f;
+          fa[m] = my_ar[m].x;
+          ref[m] = kNone;
+        }
       }
       const Tile t = tile_of(p, x);
       const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
       if (t.count > 0) {
         ok = tc::mbar_wait_spin(&bars->s_full, done & 1, abort_flag, 32);
         tc::tc_fence_after();
-        const float2 mt = meta[(im & 1) * kT + item];
-        float s[32];
-        {
-          uint32_t r32[32];
-          tc::tmem_ld32(lanes + kSCol + 32 * hh, r32);
-          tc::tmem_wait_ld();
+        // scores times the items' scales: s[j][m]
+        float s[4][8], ks[4];
+        uint32_t seen = 0;  // bit 8 j + m: row m sees item j
+        auto load_s = [&]() {
 #pragma unroll
-          for (int n = 0; n < 32; ++n) s[n] = __uint_as_float(r32[n]);
-          tc::tmem_ld32(lanes + kSCol + kR + 32 * hh, r32);
-          tc::tmem_wait_ld();
+          for (int k = 0; k < 2; ++k) {
+            uint32_t h[16], q[16];
+            tc::tmem_ld16x256_x4(lanes + ((uint32_t)(16 * k) << 16) + kSCol + 32 * hh, h);
+            tc::tmem_ld16x256_x4(lanes + ((uint32_t)(16 * k) << 16) + kSCol + kR + 32 * hh, q);
+            tc::tmem_wait_ld();
 #pragma unroll
-          for (int n = 0; n < 32; ++n) s[n] = (s[n] + __uint_as_float(r32[n])) * mt.x;
-        }
-        // rows that see this item
-        uint32_t seen = mt.y == 0.f ? 0xffffffffu : 0u;
-        if (!p.per_node && seen && (!t.entries || t.first + kT > x.n_all)) {
-          const int r = t.first + item;
-          uint32_t bits = 0;
-#pragma unroll 4
-          for (int n = 0; n < 32; ++n) {
-            bool v;
-            if (t.entries) {
-              v = r < vis[32 * hh + n].x;
-            } else if (r < x.n_win) {
-              v = x.w0 + r >= vis[32 * hh + n].y;
-            } else {
-              const int k = r - x.n_win;
-              v = (reinterpret_cast<const uint32_t*>(anc + 32 * hh + n)[k >> 5] >> (k & 31)) & 1;
-            }
-            bits |= (uint32_t)v << n;
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int m = 0; m < 8; ++m) {
+                const int r = 4 * (m >> 1) + 2 * j + (m & 1);
+                s[2 * k + j][m] = (__uint_as_float(h[r]) + __uint_as_float(q[r])) * ks[2 * k + j];
+              }
           }
-          seen = bits;
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 mt = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j];
+          ks[j] = mt.x;
+          seen |= (mt.y == 0.f ? 0xffu : 0u) << (8 * j);
         }
-        // exponents relative to the rows' references (a weight is 2^s[n])
-        const float4* ar4 = reinterpret_cast<const float4*>(row_ar + 32 * hh);
-        const float extra = fmaxf(0.f, __log2f(fabsf(mt.x)));  // a large scale counts in a weight's size
+        load_s();
+        if (!p.per_node && (!t.entries || t.first + kT > x.n_all)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = t.first + 32 * w + (lane >> 2) + 8 * j;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              bool v;
+              if (t.entries) {
+                v = r < vis[m].x;
+              } else if (r < x.n_win) {
+                v = x.w0 + r >= vis[m].y;
+              } else {
+                const int k = min(r - x.n_win, V4KV_MAX_TREE_NODES - 1);
+                v = (reinterpret_cast<const uint32_t*>(anc + m)[k >> 5] >> (k & 31)) & 1;
+              }
+              if (!v) seen &= ~(1u << (8 * j + m));
+            }
+          }
+        }
+        // exponents relative to the rows' references (a weight is 2^s)
+        float extra = 0.f;  // a large scale counts in a weight's size
+#pragma unroll
+        for (int j = 0; j < 4; ++j) extra = fmaxf(extra, fabsf(ks[j]));
+        extra = extra > 1.f ? __log2f(extra) : 0.f;
         float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 32; n += 2) {
-          const float4 f = ar4[n >> 1];
-          float e0 = fmaf(s[n], f.x, -f.y), e1 = fmaf(s[n + 1], f.z, -f.w);
-          if (!(seen >> n & 1)) e0 = -INFINITY;
-          if (!(seen >> (n + 1) & 1)) e1 = -INFINITY;
-          s[n] = e0;
-          s[n + 1] = e1;
-          top = fmaxf(top, fmaxf(e0, e1));
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int m = 0; m < 8; ++m) s[j][m] = fmaf(s[j][m], fa[m], -ref[m]);
+        if (seen != 0xffffffffu) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+              if (!(seen >> (8 * j + m) & 1)) s[j][m] = -INFINITY;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int m = 0; m < 8; ++m) top = fmaxf(top, s[j][m]);
         if (named_or(bar, top + extra > kRaise || !ok)) {
           if (named_or(bar, !ok)) {
             ok = false;
             break;
           }
-          // raise the references to the rows' maxima so far, O^T and the sums with them
-          // (the scores are taken from S again: a reference of kNone has swallowed them)
-          float u[32];
-          {
-            uint32_t r32[32], q32[32];
-            tc::tmem_ld32(lanes + kSCol + 32 * hh, r32);
-            tc::tmem_ld32(lanes + kSCol + kR + 32 * hh, q32);
-            tc::tmem_wait_ld();
+          // raise the references to the rows' maxima so far, O^T and the sums
+          // with them (the scores are taken from S again: a reference of kNone
+          // has swallowed them)
+          load_s();
 #pragma unroll
-            for (int n = 0; n < 32; n += 2) {
-              const float4 f = ar4[n >> 1];
-              const float y0 = (__uint_as_float(r32[n]) + __uint_as_float(q32[n])) * mt.x;
-              const float y1 = (__uint_as_float(r32[n + 1]) + __uint_as_float(q32[n + 1])) * mt.x;
-              s[n] = (seen >> n & 1) ? y0 * f.x : -INFINITY;
-              s[n + 1] = (seen >> (n + 1) & 1) ? y1 * f.z : -INFINITY;
-              u[n] = s[n] + extra;
-              u[n + 1] = s[n + 1] + extra;
+          for (int m = 0; m < 8; ++m) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[j][m] = (seen >> (8 * j + m) & 1) ? s[j][m] * fa[m] : -INFINITY;
+              mx = fmaxf(mx, s[j][m]);
             }
-          }
-          const float mx = reduce_scatter32<true>(u, lane);
-          red[32 * w + lane] = mx;
-          named_sync(bar);
-          if (w == 0) {
-            float nm = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
-            const float old = row_ar[32 * hh + lane].y;
-            nm = fmaxf(nm, old);
-            row_ar[32 * hh + lane].y = nm;
-            fac[lane] = exp2f(old - nm);
+            mx += extra;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane < 4) red[32 * w + 8 * c4 + m] = mx;
           }
           named_sync(bar);
 #pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            l[n] *= fac[n];
-            s[n] -= row_ar[32 * hh + n].y;
+          for (int m = 0; m < 8; ++m) {
+            const int n = 8 * c4 + m;
+            const float nm = fmaxf(fmaxf(fmaxf(red[n], red[32 + n]), fmaxf(red[64 + n], red[96 + n])), ref[m]);
+            const float f = exp2f(ref[m] - nm);
+            ref[m] = nm;
+            l[m] *= f;
+            if (w == 0 && lane < 4) {
+              fac[n] = f;
+              my_ar[m].y = nm;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j][m] -= nm;
           }
+          named_sync(bar);
           if (any) {
             // S is complete, so the last tile's product into O^T is
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t r32[32];
-              tc::tmem_ld32(lanes + kOCol + kR * c + 32 * hh, r32);
+            for (int g = 0; g < 16; ++g) {
+              const uint32_t at = lanes + kOCol + kR * (g >> 2) + 32 * hh + 8 * (g & 3);
+              uint32_t r8[8];
+              tmem_ld8(at, r8);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int n = 0; n < 32; ++n) r32[n] = __float_as_uint(__uint_as_float(r32[n]) * fac[n]);
-              tc::tmem_st32(lanes + kOCol + kR * c + 32 * hh, r32);
+              for (int n = 0; n < 8; ++n) r8[n] = __float_as_uint(__uint_as_float(r8[n]) * fac[8 * (g & 3) + n]);
+              tmem_st8(at, r8);
             }
             tc::tmem_wait_st();
           }
         }
         any = true;
-        // weights of the items' codes, their block exponents, and the two terms
-        uint32_t mine = 0;
-        uint8_t* prow = sm + kPOff;
+        // weights of the items' codes
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t hw[4], lw[4];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[4];
+          for (int m = 0; m < 8; ++m) {
+            const float pr = fast_exp2(s[j][m]);
+            l[m] += pr;
+            s[j][m] = pr * ks[j];
+          }
+        if (seen != 0xffffffffu) {  // 0 * NaN
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int n = 16 * g + 4 * q + e;
-              const float pr = fast_exp2(s[n]);
-              l[n] += pr;
-              const float pw = (seen >> n & 1) ? pr * mt.x : 0.f;
-              // largest exponent of the 32 items, as the block scale's byte for [2^7, 2^8)
-              const uint32_t b = max(__reduce_max_sync(0xffffffffu, __float_as_uint(pw) & 0x7fffffffu) >> 23, 16u);
-              if (lane == n) mine = b - 7u;
-              v[e] = pw * __uint_as_float((261u - b) << 23);
-            }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+              if (!(seen >> (8 * j + m) & 1)) s[j][m] = 0.f;
+        }
+        // largest magnitude of the 32 items per row: the upper halves of two
+        // rows' bits in a word (the exponent and seven bits, which order alike)
+        uint32_t bytes[2] = {0, 0};
+        float mul[8];
+#pragma unroll
+        for (int m = 0; m < 8; m += 2) {
+          uint32_t e = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            e = __vmaxu2(e, __byte_perm(__float_as_uint(s[j][m]), __float_as_uint(s[j][m + 1]), 0x7632) & 0x7fff7fffu);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) e = __vmaxu2(e, __shfl_xor_sync(0xffffffffu, e, o));
+          const uint32_t b0 = max((e & 0xffffu) >> 7, 16u), b1 = max(e >> 23, 16u);
+          // into [2^7, 2^8), and the block scale's byte that undoes it
+          mul[m] = __uint_as_float((261u - b0) << 23);
+          mul[m + 1] = __uint_as_float((261u - b1) << 23);
+          bytes[m >> 2] |= ((b0 - 7u) | ((b1 - 7u) << 8)) << (16 * ((m >> 1) & 1));
+        }
+        sf[4 * (8 * c4 + (lane >> 2)) + w] = (uint8_t)((lane & 16 ? bytes[1] : bytes[0]) >> (8 * ((lane >> 2) & 3)));
+        // the two terms of four items, eight rows each
+        const uint32_t pcol = 2 * hh + (c4 >> 1), pbyte = 8 * (c4 & 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hw[2], lw[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
             uint32_t h0, h1, l0, l1;
-            split2(v[0], v[1], h0, l0);
-            split2(v[2], v[3], h1, l1);
+            split2(s[j][4 * q] * mul[4 * q], s[j][4 * q + 1] * mul[4 * q + 1], h0, l0);
+            split2(s[j][4 * q + 2] * mul[4 * q + 2], s[j][4 * q + 3] * mul[4 * q + 3], h1, l1);
             hw[q] = h0 | (h1 << 16);
             lw[q] = l0 | (l1 << 16);
           }
-          *reinterpret_cast<uint4*>(prow + tc::sw128_off(item, 2 * hh + g)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(prow + tc::sw128_off(item, 4 + 2 * hh + g)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          const int item = 32 * w + (lane >> 2) + 8 * j;
+          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, pcol) + pbyte) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, 4 + pcol) + pbyte) = make_uint2(lw[0], lw[1]);
         }
-        sf[4 * lane + w] = (uint8_t)mine;
         named_sync(bar);
         const uint32_t word = reinterpret_cast<const uint32_t*>(sf)[lane];
         tmem_st1(lanes + kSfHi + hh, word);
@@ -843,7 +1013,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         tc::mbar_arrive(&bars->p_full);
-        im += t.images;
         ++done;
       }
       if (seg_last) {
@@ -855,11 +1024,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         tc::tc_fence_after();
         ++seg;
         // the rows' sums over all items
-        {
-          float t32[32];
 #pragma unroll
-          for (int n = 0; n < 32; ++n) t32[n] = l[n];
-          red[32 * w + lane] = reduce_scatter32<false>(t32, lane);
+        for (int m = 0; m < 8; ++m) {
+          float sum = l[m];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane < 4) red[32 * w + 8 * c4 + m] = sum;
         }
         named_sync(bar);
         const bool whole = seg_tile0 == 0 && x.tile + 1 == x.q.te + x.q.tr;
@@ -871,40 +1041,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           if (!whole) p.w.part_ml[slot * kR + 32 * hh + lane] = make_float2(row_ar[32 * hh + lane].y, sum);
         }
         named_sync(bar);
-        const float2* rope = p.w.rope;
+        // O^T: lane = dim 128 c + 32 w + lane, column = row
+        if (!whole) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r32[32];
-          tc::tmem_ld32(lanes + kOCol + kR * c + 32 * hh, r32);
-          tc::tmem_wait_ld();
-          const int d = 128 * c + item, pair = ((d & ~1) - a.rope.rope_offset) >> 1;
-          const bool rot = whole && d >= a.rope.rope_offset && d < a.rope.rope_offset + a.rope.rope_dim;
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r32[32];
+            tc::tmem_ld32(lanes + kOCol + kR * c + 32 * hh, r32);
+            tc::tmem_wait_ld();
+            float* o = p.w.part_o + (slot * kR + 32 * hh) * kD + 128 * c + 32 * w + lane;
 #pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            float v = any ? __uint_as_float(r32[n]) * fac[n] : 0.f;
-            const float other = __shfl_xor_sync(0xffffffffu, v, 1);
-            const int row = 32 * hh + n;
-            if (row >= x.nrows) continue;
-            if (!whole) {
-              p.w.part_o[(slot * kR + row) * kD + d] = v;
-              continue;
-            }
-            if (rot) {
-              const int node = (int)((x.row0 + row) / a.heads);
-              float cs, sn;
-              if (pair < kPairs) {
-                const float2 f = rope[(size_t)node * kPairs + pair];
-                cs = f.x;
-                sn = f.y;
-              } else {
-                rope_cs(a.rope, pair, (long long)x.q.L + p.w.depth[node], &cs, &sn);
+            for (int n = 0; n < 32; ++n)
+              if (32 * hh + n < x.nrows) o[n * kD] = any ? __uint_as_float(r32[n]) : 0.f;
+          }
+        } else {
+          // rows of bf16 in Q's place (its products are done), half hh's 32 KB
+          // of it, then one copy of the rows, which are consecutive in `out`
+          uint8_t* stage = sm + kQOff + 32768 * hh;
+          const int4* row_vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int d = 128 * c + 32 * w + lane, pair = (d - a.rope.rope_offset) >> 1;
+            const bool rot = d >= a.rope.rope_offset && d < a.rope.rope_offset + a.rope.rope_dim;
+            const bool any_rot = __any_sync(0xffffffffu, rot);
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              uint32_t r8[8];
+              float v[8];
+              tmem_ld8(lanes + kOCol + kR * c + 32 * hh + 8 * g, r8);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int n = 0; n < 8; ++n) v[n] = any ? __uint_as_float(r8[n]) * fac[8 * g + n] : 0.f;
+              if (any_rot) {
+                float cs = 1.f, sn = 0.f;
+                int have = -1;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                  const float other = __shfl_xor_sync(0xffffffffu, v[n], 1);
+                  const int node = row_vis[8 * g + n].z;
+                  if (rot) {
+                    if (node != have) {
+                      have = node;
+                      if (pair < kPairs) {
+                        const float2 f = p.w.rope[(size_t)node * kPairs + pair];
+                        cs = f.x;
+                        sn = f.y;
+                      } else {
+                        rope_cs(a.rope, pair, (long long)x.q.L + p.w.depth[node], &cs, &sn);
+                      }
+                    }
+                    v[n] = (d & 1) ? __fadd_rn(__fmul_rn(other, -sn), __fmul_rn(v[n], cs))
+                                   : __fsub_rn(__fmul_rn(v[n], cs), __fmul_rn(other, -sn));
+                  }
+                }
               }
-              v = (d & 1) ? __fadd_rn(__fmul_rn(other, -sn), __fmul_rn(v, cs))
-                          : __fsub_rn(__fmul_rn(v, cs), __fmul_rn(other, -sn));
+              // even lanes store a pair of dims of rows 2 k, odd lanes of rows 2 k + 1
+#pragma unroll
+              for (int n = 0; n < 8; n += 2) {
+                const float give = lane & 1 ? v[n] : v[n + 1];
+                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                const uint32_t w2 = lane & 1 ? float_to_bf16_bits(got) | ((uint32_t)float_to_bf16_bits(v[n + 1]) << 16)
+                                             : float_to_bf16_bits(v[n]) | ((uint32_t)float_to_bf16_bits(got) << 16);
+                *reinterpret_cast<uint32_t*>(stage + (8 * g + n + (lane & 1)) * (2 * kD) + 2 * (d & ~1)) = w2;
+              }
             }
-            a.out[(size_t)(x.row0 + row) * kD + d] = float_to_bf16_bits(v);
+          }
+          tc::fence_proxy_async_smem();
+          named_sync(bar);
+          const int rows = min(32, x.nrows - 32 * hh);
+          if (w == 0 && lane == 0 && rows > 0) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                             a.out + (size_t)(x.row0 + 32 * hh) * kD),
+                         "r"(sbase + kQOff + 32768 * hh), "r"(rows * 2 * kD)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
         }
+        if (w == 0 && lane == 0) tc::mbar_arrive(&bars->epi);
         named_sync(bar);  // fac and the references are free
         seg_open = true;
       }
@@ -1128,7 +1341,13 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   p.per_node = a.topk != nullptr || a.heads % kR == 0;
   p.hc = (a.heads + kR - 1) / kR;
   layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.total_nodes, p.grid);
-  cudaError_t e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaSuccess;
+  p.pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64;
+  if (p.pages) {
+    e = encode_cols_u8(&p.map, a.main.data, (uint64_t)a.main.num_pages * a.main.spb, kD, 128, 64);
+    if (e != cudaSuccess) return e;
+  }
+  e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1), dim3(256), 0, stream, p);
