@@ -433,7 +433,7 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
   st = check_device(&sms);
   if (st != V4KV_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < tree_workspace_bytes(batch, heads, total_nodes, max_nodes, sms))
+      workspace_bytes < tree_workspace_bytes(batch, heads, total_nodes, topk ? k : 0, window_len, max_seq_len, sms))
     return V4KV_ERR_INVALID_ARG;
   if (empty) return V4KV_OK;
   TreeArgs a{};
@@ -472,7 +472,7 @@ v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total
   int sms = 0;
   v4kv_status st = check_device(&sms);
   if (st != V4KV_OK) return st;
-  *bytes = tree_workspace_bytes(batch, heads, total_nodes, max_nodes, sms);
+  *bytes = tree_workspace_bytes(batch, heads, total_nodes, k, window_len, max_seq_len, sms);
   return V4KV_OK;
 }
 

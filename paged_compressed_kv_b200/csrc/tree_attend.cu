@@ -30,9 +30,11 @@
 // The normaliser and the running reference are fp32. With block scales P needs
 // no fixed range, so the reference moves only when a score passes it by 2^40.
 //
-// Warps: 0-7 softmax (a thread has 4 items of the tile and 8 of the rows; also
-// the unit's Q and its epilogue), 8-11 load tiles, 12 issues the MMAs, 13 and
-// 14 resolve the even and odd tiles' row addresses ahead.
+// Warps: 0-7 softmax (a thread has 4 items of the tile and 8 of the rows) and
+// the unit's epilogue, 8-11 load tiles, 12 issues the MMAs, 13 and 14 resolve
+// the even and odd tiles' row addresses ahead, 15 loads the units' Q. The prep
+// kernel has written every Q as the image its products read, and every raw row
+// as its two terms, once for all units that use it.
 //
 // Schedule: the tiles of all units are one list; the prep kernel gives each
 // block of the grid (one per SM) an equal share by estimated cost. A block that
@@ -49,11 +51,12 @@ namespace {
 constexpr int kR = 64;    // rows of a unit
 constexpr int kT = 128;   // items of a tile
 constexpr int kD = 512;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;
 constexpr int kRing = 4;  // tiles whose rows are resolved ahead
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr float kRaise = 40.f;   // log2 by which a score may pass its reference
-constexpr int kPairs = kRopeTable;
+constexpr int kPairs = 256;     // rotated pairs of a row at most
+constexpr int kPrepRows = 4;    // rows a warp of the prep kernel splits
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr uint32_t kQOff = 0;                 // 4 x [128 rows (64 hi, 64 lo) x 128 dims]
@@ -61,16 +64,16 @@ constexpr uint32_t kVOff = 65536;             // 2 stages of 4 x [128 items x 12
 constexpr uint32_t kStage = 65536;
 constexpr uint32_t kChunk = 16384;
 constexpr uint32_t kPOff = 196608;            // [128 items x (64 hi, 64 lo)]
-constexpr uint32_t kMetaOff = 212992;         // [kRing][128] {scale, 0 or -inf}
-constexpr uint32_t kPtrOff = kMetaOff + kRing * 1024;  // [kRing][128] row addresses, bit 0: fp8
-constexpr uint32_t kRowOff = kPtrOff + kRing * 1024; // [64] {score factor, reference}
+constexpr uint32_t kMetaOff = 212992;         // [kRing][128] {scale, log2 |scale|, 1 / |scale|, 0 or -inf}
+constexpr uint32_t kPtrOff = kMetaOff + kRing * 2048;  // [kRing][128] row addresses
+constexpr uint32_t kRowOff = kPtrOff + kRing * 1024; // [64] the rows' references
 constexpr uint32_t kAncOff = kRowOff + 512;   // [64] ancestors of the row's node, 128 bits
 constexpr uint32_t kVisOff = kAncOff + 1024;  // [64] {visible entries, first visible token, node}
 constexpr uint32_t kRedOff = kVisOff + 1024;   // [8][32] reductions over a warp's items
 constexpr uint32_t kSfOff = kRedOff + 1024;   // [64] block scales of P, a byte per 32 items
 constexpr uint32_t kFacOff = kSfOff + 256;    // [64] per-row factors
 constexpr uint32_t kBarOff = kFacOff + 256;
-constexpr uint32_t kMiscOff = kBarOff + 192;
+constexpr uint32_t kMiscOff = kBarOff + 256;
 constexpr uint32_t kSmemBytes = kMiscOff + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
@@ -85,17 +88,21 @@ constexpr uint32_t kSfLo = 400;
 constexpr uint32_t kCols = 512;
 
 struct Bars {
-  uint64_t kv_full[2], kv_empty[2];
+  uint64_t kv_full[2][4], kv_empty[2][4];  // per stage and 128 dims
   uint64_t addr_full[kRing], addr_free[kRing];
-  uint64_t q_full, s_full, p_full, pv_done, epi, drain;
+  uint64_t q_full, q_empty, s_full, s_free, p_full, p_free, pv_done, drain;
 };
-static_assert(sizeof(Bars) <= 192, "barrier area");
+static_assert(sizeof(Bars) <= 256, "barrier area");
 
 // What the prep kernel leaves in the workspace.
 struct TreeWs {
   uint4* anc;         // [total_nodes] the node and its ancestors, a bit each
   int32_t* depth;     // [total_nodes]
-  float2* rope;       // [total_nodes][kPairs] cos, sin at the node's position
+  float2* rope;       // [total_nodes][rope_dim / 2] cos, sin at the node's position
+  uint8_t* q;         // the units' Q as shared-memory images, 64 KB each
+  float* q_factor;    // their rows' score factors, 64 each
+  uint8_t* raw;       // rows of the windows and trees as two e4m3 terms, 512 bytes each
+  float2* raw_meta;   // their {scale, 0 or -inf: no such row}
   long long* cost;    // [batch + 1] prefix sums over sequences
   int32_t* tiles;     // [batch + 1]
   int4* rec;          // [grid + 1] a block's first tile: {index, sequence, unit in it, tile in that}
@@ -107,8 +114,11 @@ struct Params {
   TreeArgs a;
   TreeWs w;
   int grid;
+  int ratio_log, spb_log;  // of main_cache
   int hc;        // units per node (per_node)
   int per_node;  // a unit's rows belong to one node
+  int raw_blocks;  // prep blocks per sequence for its raw rows
+  int max_units;   // units of a sequence at most
   int pages;     // tiles of entries are whole pages of 64 rows, loaded by TMA
   CUtensorMap map;  // boxes of 64 rows x 128 bytes of main_cache
 };
@@ -123,6 +133,21 @@ struct SeqPlan {
   int L, units, te, tr;
 };
 
+// The raw rows of a sequence in the workspace, consecutive: the cached tokens
+// that any node sees, then the nodes.
+__device__ __forceinline__ size_t raw_row0(const TreeArgs& a, const SeqPlan& q, int b) {
+  return (size_t)b * min(a.window_len - 1, a.max_len) + q.s.first;
+}
+__device__ __forceinline__ int raw_w0(const TreeArgs& a, const SeqPlan& q) {
+  return min(q.L, max(0, q.L + 1 - a.window_len));
+}
+
+// Index of a unit's Q image. Distinct: a sequence's units are at most one more
+// than its rows fill.
+__device__ __forceinline__ int q_image(const Params& p, const SeqPlan& q, int b, int u) {
+  return p.per_node ? q.s.first * p.hc + u : b + (int)((long long)q.s.first * p.a.heads / kR) + u;
+}
+
 constexpr int kCostFp8 = 4, kCostTwo = 8, kCostSeg = 4;
 
 __device__ __forceinline__ SeqPlan plan_of(const Params& p, int b, int32_t* st) {
@@ -132,7 +157,7 @@ __device__ __forceinline__ SeqPlan plan_of(const Params& p, int b, int32_t* st) 
   q.L = seq_len(a, b);
   const int n = q.s.n;
   q.units = p.per_node ? n * p.hc : (n * a.heads + kR - 1) / kR;
-  const int seen = max(0, q.L + n - a.window_len) / a.ratio;  // by the deepest node there can be
+  const int seen = max(0, q.L + n - a.window_len) >> p.ratio_log;  // by the deepest node there can be
   q.te = ((a.topk ? a.k : seen) + kT - 1) / kT;
   const int raw = p.per_node ? min(q.L + n, a.window_len) : min(q.L, a.window_len - 1) + n;
   q.tr = (raw + kT - 1) / kT;
@@ -173,7 +198,7 @@ __device__ __forceinline__ void unit_set(const Params& p, Unit& x) {
     x.nrows = min(kR, a.heads - h0);
     x.row0 = (long long)(x.q.s.first + i) * a.heads + h0;
     const int d = p.w.depth[x.q.s.first + i];
-    x.n_ent = a.topk ? a.k : max(0, L + d + 1 - W) / a.ratio;
+    x.n_ent = a.topk ? a.k : max(0, L + d + 1 - W) >> p.ratio_log;
     x.n_all = x.n_ent;
     x.w0 = min(L, max(0, L + d + 1 - W));
     x.n_win = L - x.w0;
@@ -190,8 +215,8 @@ __device__ __forceinline__ void unit_set(const Params& p, Unit& x) {
       lo = min(lo, d);
       hi = max(hi, d);
     }
-    x.n_ent = max(0, L + hi + 1 - W) / a.ratio;
-    x.n_all = max(0, L + lo + 1 - W) / a.ratio;
+    x.n_ent = max(0, L + hi + 1 - W) >> p.ratio_log;
+    x.n_all = max(0, L + lo + 1 - W) >> p.ratio_log;
     x.w0 = min(L, max(0, L + lo + 1 - W));
     x.n_win = L - x.w0;
     x.n_tree = last + 1;
@@ -199,7 +224,7 @@ __device__ __forceinline__ void unit_set(const Params& p, Unit& x) {
 }
 
 // next unit (after the last: b == batch)
-__device__ __forceinline__ void unit_next(const Params& p, Unit& x) {
+__device__ __noinline__ void unit_next(const Params& p, Unit& x) {
   ++x.u;
   x.tile = 0;
   while (x.u >= x.q.units) {
@@ -332,41 +357,78 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 
 // ------------------------------------------------------------------ loading (warps 8-11)
 
+// what the softmax needs of an item: its scale, and for the weight of its raw
+// codes log2 |scale| and 1 / |scale|. A zero scale stands for zero codes (the
+// item still counts in the normaliser), one that is not finite for NaN.
+__device__ __forceinline__ float4 item_meta(float scale, bool there) {
+  if (!there) return make_float4(0.f, 0.f, 0.f, -INFINITY);
+  if (!isfinite(scale)) return make_float4(__int_as_float(0x7fffffff), 0.f, 1.f, 0.f);
+  const float m = fabsf(scale);
+  return m == 0.f ? make_float4(0.f, 0.f, 1.f, 0.f) : make_float4(scale, log2f(m), 1.f / m, 0.f);
+}
+
 // Lane l resolves items l, l + 32, l + 64, l + 96 of a tile: their rows'
-// addresses (bit 0: fp8 codes; 0: no such item) and scales. The loads go in
-// phases (top-k entry, block table, scale), the four of a phase independent of
-// one another.
+// addresses (0: no such item) and scales. The loads go in phases (top-k entry,
+// block table, scale), the four of a phase independent of one another.
 __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, const Tile& t, int lane,
-                                             unsigned long long* rows, float2* meta) {
+                                             unsigned long long* rows, float4* meta) {
   const TreeArgs& a = p.a;
-  int j[4], pg[4], err = 0;
-  bool tree[4];
-  const bool main = t.entries;
-  const PoolArgs& pool = main ? a.main : a.window;
+  if (!t.entries) {
+    const size_t base = raw_row0(a, x.q, x.b);
+    const int w0 = raw_w0(a, x.q);
+    const uint4 m4 = p.w.anc[x.q.s.first + x.node0];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int k = lane + 32 * r;
+      int n = t.first + k;
+      unsigned long long at = 0;
+      float2 mt = make_float2(0.f, -INFINITY);
+      if (k < t.count) {
+        if (n < x.n_win) {
+          n += x.w0 - w0;
+        } else {
+          n -= x.n_win;
+          if (p.per_node) {  // the n-th of the node's ancestors
+            uint32_t m = m4.x;
+            int up = 0;
+            if (n >= __popc(m)) { n -= __popc(m); m = m4.y; up = 32; }
+            if (up == 32 && n >= __popc(m)) { n -= __popc(m); m = m4.z; up = 64; }
+            if (up == 64 && n >= __popc(m)) { n -= __popc(m); m = m4.w; up = 96; }
+            for (; n > 0; --n) m &= m - 1;
+            n = up + __ffs(m) - 1;
+          }
+          n += x.q.L - w0;
+        }
+        at = reinterpret_cast<unsigned long long>(p.w.raw) + (base + n) * (2 * kD);
+        mt = p.w.raw_meta[base + n];
+      }
+      rows[k] = at;
+      meta[k] = item_meta(mt.x, mt.y == 0.f);
+    }
+    return;
+  }
+  const PoolArgs& pool = a.main;
   const int32_t* bt = pool.block_table + (size_t)x.b * pool.max_blocks;
+  int j[4], pg[4], err = 0;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int k = lane + 32 * r;
     j[r] = k < t.count ? t.first + k : -1;
-    tree[r] = !main && j[r] >= x.n_win;
-    if (main && a.topk && j[r] >= 0) j[r] = a.topk[(size_t)(x.q.s.first + x.node0) * a.k + j[r]];
+    if (a.topk && j[r] >= 0) j[r] = a.topk[(size_t)(x.q.s.first + x.node0) * a.k + j[r]];
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     pg[r] = -1;
-    if (tree[r] || j[r] < 0) continue;
-    if (main && a.topk && j[r] >= (x.q.L + a.ratio - 1) / a.ratio) {
+    if (j[r] < 0) continue;
+    if (a.topk && j[r] >= (x.q.L + a.ratio - 1) >> p.ratio_log) {
       err |= V4KV_DEV_BAD_INDEX;
       j[r] = -1;
-      continue;
-    }
-    if (!main) j[r] += x.w0;
-    if (j[r] / pool.spb >= pool.max_blocks) {
+    } else if (j[r] >> p.spb_log >= pool.max_blocks) {
       err |= V4KV_DEV_BAD_SLOT;
       j[r] = -1;
-      continue;
+    } else {
+      pg[r] = bt[j[r] >> p.spb_log];
     }
-    pg[r] = bt[j[r] / pool.spb];
   }
   const bool fp8 = pool.dtype == V4KV_FP8_E4M3;
   float scale[4];
@@ -376,32 +438,18 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
     scale[r] = 1.f;
     at[r] = 0;
     if (j[r] < 0) continue;
-    if (tree[r]) {
-      int n = j[r] - x.n_win;
-      if (p.per_node) {  // the n-th of the node's ancestors
-        const uint4 m4 = p.w.anc[x.q.s.first + x.node0];
-        uint32_t m = m4.x;
-        int base = 0;
-        if (n >= __popc(m)) { n -= __popc(m); m = m4.y; base = 32; }
-        if (base == 32 && n >= __popc(m)) { n -= __popc(m); m = m4.z; base = 64; }
-        if (base == 64 && n >= __popc(m)) { n -= __popc(m); m = m4.w; base = 96; }
-        for (; n > 0; --n) m &= m - 1;
-        n = base + __ffs(m) - 1;
-      }
-      at[r] = reinterpret_cast<unsigned long long>(a.k_tree + (size_t)(x.q.s.first + n) * kD);
-    } else if (pg[r] < 0 || pg[r] >= pool.num_pages) {
+    if (pg[r] < 0 || pg[r] >= pool.num_pages) {
       err |= V4KV_DEV_BAD_PAGE;
     } else {
-      const size_t slot = (size_t)pg[r] * pool.spb + j[r] % pool.spb;
+      const size_t slot = ((size_t)pg[r] << p.spb_log) + (j[r] & (pool.spb - 1));
       if (fp8) scale[r] = pool.scales[slot];
-      at[r] = reinterpret_cast<unsigned long long>(pool.data) + slot * (fp8 ? kD : 2 * kD) + (fp8 ? 1 : 0);
+      at[r] = reinterpret_cast<unsigned long long>(pool.data) + slot * (fp8 ? kD : 2 * kD);
     }
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     rows[lane + 32 * r] = at[r];
-    meta[lane + 32 * r] = at[r] ? make_float2(isfinite(scale[r]) ? scale[r] : __int_as_float(0x7fffffff), 0.f)
-                                : make_float2(0.f, -INFINITY);
+    meta[lane + 32 * r] = item_meta(scale[r], at[r] != 0);
   }
   if (err) flag(a.dev_status, err);
 }
@@ -425,48 +473,53 @@ __device__ __forceinline__ uint32_t amax_bf16(const uint4* r) {
   return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16;
 }
 
-// kN rows, the whole warp: lane takes dims 16 lane .. 16 lane + 15 of each;
-// all loads are in flight together
-template <int kN>
-__device__ __forceinline__ void load_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
-                                          uint8_t* lo_dst, float2* meta) {
-  uint4 raw[kN][2];
-#pragma unroll
-  for (int k = 0; k < kN; ++k) {
-    const unsigned long long row = rows[k];
-    const uint4* p = reinterpret_cast<const uint4*>(row & ~1ull);
-    raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
-    if (row) {
-      raw[k][0] = p[row & 1 ? lane : 2 * lane];
-      if (!(row & 1)) raw[k][1] = p[2 * lane + 1];
-    }
+// a lane's 16 dims of a bf16 row as two terms; the row's scale (NaN, and zero
+// terms, for a row that is not finite)
+__device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& lo) {
+  const uint32_t m = amax_bf16(raw);
+  if (m >= 0x7f800000u) {
+    hi = lo = make_uint4(0, 0, 0, 0);
+    return __int_as_float(0x7fffffff);
   }
+  float v[16];
+  bf16x16(raw, v);
+  split16(v, scale_up(m), hi, lo);
+  return scale_down(m);
+}
+
+// 32 bf16 rows, the whole warp: lane takes dims 16 lane .. 16 lane + 15 of each;
+// the next rows' loads fly while two are split
+__device__ __noinline__ void load_bf16_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
+                                            uint8_t* lo_dst, float4* meta) {
+  auto get = [&](int r, uint4* raw) {
+    const uint4* p = reinterpret_cast<const uint4*>(r < 32 ? rows[r] : 0ull);
+    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+    if (p) {
+      raw[0] = p[2 * lane];
+      raw[1] = p[2 * lane + 1];
+    }
+  };
+  uint4 raw[8][2];
 #pragma unroll
-  for (int k = 0; k < kN; ++k) {
-    const unsigned long long row = rows[k];
-    const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r0 + k, lane & 7);
-    uint4 hi = raw[k][0], lo = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    bool bad, set = false;
-    if (row & 1) {
-      bad = __any_sync(0xffffffffu, has_nan_code(hi));
-    } else {
-      const uint32_t m = amax_bf16(raw[k]);
-      bad = m >= 0x7f800000u;
-      float v[16];
-      bf16x16(raw[k], v);
-      split16(v, scale_up(m), hi, lo);
-      scale = scale_down(m);
-      set = row != 0;
+  for (int k = 0; k < 6; ++k) get(k, raw[k]);
+#pragma unroll 1
+  for (int r = 0; r < 32; r += 2) {
+    get(r + 6, raw[6]);
+    get(r + 7, raw[7]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r0 + r + k, lane & 7);
+      uint4 hi, lo;
+      const float scale = split_row(raw[k], hi, lo);
+      if (rows[r + k] && lane == 0) meta[r0 + r + k] = item_meta(scale, true);
+      *reinterpret_cast<uint4*>(hi_dst + off) = hi;
+      *reinterpret_cast<uint4*>(lo_dst + off) = lo;
     }
-    if (bad) {
-      hi = lo = make_uint4(0, 0, 0, 0);
-      scale = __int_as_float(0x7fffffff);
-      set = true;
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      raw[k][0] = raw[k + 2][0];
+      raw[k][1] = raw[k + 2][1];
     }
-    if (set && lane == 0) meta[r0 + k].x = scale;
-    *reinterpret_cast<uint4*>(hi_dst + off) = hi;
-    if (lo_dst) *reinterpret_cast<uint4*>(lo_dst + off) = lo;
   }
 }
 
@@ -481,27 +534,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   uint8_t* sm = smem_raw + pad;
   const uint32_t sbase = raw_addr + pad;
   Bars* bars = reinterpret_cast<Bars*>(sm + kBarOff);
-  float2* meta = reinterpret_cast<float2*>(sm + kMetaOff);
-  float2* row_ar = reinterpret_cast<float2*>(sm + kRowOff);
+  float4* meta = reinterpret_cast<float4*>(sm + kMetaOff);
+  float* row_ref = reinterpret_cast<float*>(sm + kRowOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kMiscOff + 4);
   const TreeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&bars->kv_full[s], 128);
-      tc::mbar_init(&bars->kv_empty[s], 1);
+    for (int s = 0; s < 8; ++s) {
+      tc::mbar_init(&bars->kv_full[s >> 2][s & 3], 4);
+      tc::mbar_init(&bars->kv_empty[s >> 2][s & 3], 1);
     }
     for (int s = 0; s < kRing; ++s) {
       tc::mbar_init(&bars->addr_full[s], 32);
       tc::mbar_init(&bars->addr_free[s], 1);
     }
-    tc::mbar_init(&bars->q_full, 256);
+    tc::mbar_init(&bars->q_full, 1);
+    tc::mbar_init(&bars->q_empty, 1);
     tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->p_full, 256);
+    tc::mbar_init(&bars->s_free, 8);
+    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->p_free, 1);
     tc::mbar_init(&bars->pv_done, 1);
-    tc::mbar_init(&bars->epi, 2);
     tc::mbar_init(&bars->drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -526,7 +581,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   x.q = plan_of(p, x.b, nullptr);
   unit_set(p, x);
 
-  if (warp >= 13) {
+  if (warp == 15) {
+    // ======================= the units' Q, as their last one's products are done
+    bool ok = true;
+    uint32_t seg = 0;
+    for (int i = 0; i < n_tiles && ok; ++seg) {
+      if (seg > 0) ok = tc::mbar_wait(&bars->q_empty, (seg - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&bars->q_full, 65536);
+        const uint8_t* src = p.w.q + (size_t)q_image(p, x.q, x.b, x.u) * 65536;
+        for (int k = 0; k < 4; ++k)
+          tc::bulk_load(sbase + kQOff + k * 16384, src + k * 16384, 16384, &bars->q_full);
+      }
+      i += x.q.te + x.q.tr - x.tile;
+      if (i < n_tiles) unit_next(p, x);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      flag(a.dev_status, V4KV_DEV_TIMEOUT);
+    }
+    // the last copy has landed before the block's shared memory is released
+    volatile int never = 0;
+    if (seg > 0 && !tc::mbar_wait(&bars->q_full, (seg - 1) & 1, &never)) flag(a.dev_status, V4KV_DEV_TIMEOUT);
+  } else if (warp >= 13) {
     // ======================= row addresses and scales, up to kRing tiles ahead.
     // Tile number `done` of the block (tiles without items do not count) is in
     // slot done % kRing.
@@ -556,60 +637,82 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     const int w = warp - 8;
     bool ok = true;
     uint32_t im = 0, done = 0;
+    auto wait_empty = [&](uint32_t m, int c) {
+      return m < 2 || tc::mbar_wait(&bars->kv_empty[m & 1][c], ((m - 2) >> 1) & 1, abort_flag);
+    };
     for (int i = 0; i < n_tiles && ok; ++i) {
       const Tile t = tile_of(p, x);
       if (t.count > 0) {
         const uint32_t s = im & 1, slot = done % kRing;
+        const unsigned long long* rows = reinterpret_cast<const unsigned long long*>(sm + kPtrOff) + slot * kT;
         ok = tc::mbar_wait(&bars->addr_full[slot], (done / kRing) & 1, abort_flag);
-        for (int k = 0; k < t.images; ++k)
-          if (im + k >= 2) ok = ok && tc::mbar_wait(&bars->kv_empty[(im + k) & 1], ((im + k - 2) >> 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const unsigned long long* rows = reinterpret_cast<const unsigned long long*>(sm + kPtrOff) + slot * kT + 32 * w;
-        float2* mt = meta + slot * kT;
-        uint8_t* dst = sm + kVOff + s * kStage;
-        if (t.images == 1) {
-          if (p.pages && t.first + kT <= x.n_all) {
-            // two whole pages, every row of them visible: eight boxes
-            if (w == 0 && lane == 0) tc::mbar_arrive_expect_tx(&bars->kv_full[s], kStage);
-            if (w == 0) {
-              __syncwarp();
-              if (lane < 8) {
-                const unsigned long long row = rows[64 * (lane >> 2)];
-                // a page that is missing is read behind the pool's end: zeros
-                const int y = row ? (int)(((row & ~1ull) - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
-                                  : a.main.num_pages * a.main.spb;
-                tc::tma_load_2d(sbase + kVOff + s * kStage + (lane & 3) * kChunk + (lane >> 2) * (kChunk / 2), &p.map,
-                                128 * (lane & 3), y, &bars->kv_full[s]);
-              }
+        if (t.images == 1 && p.pages && t.first + kT <= x.n_all) {
+          // two whole pages, every row of them visible: two boxes per 128 dims,
+          // as the last tile's product leaves them
+          int y = 0;
+          if (lane < 2) {
+            // a page that is missing is read behind the pool's end: zeros
+            const unsigned long long row = rows[64 * lane];
+            y = row ? (int)((row - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
+                    : a.main.num_pages * a.main.spb;
+          }
+          for (int c = 0; c < 4 && ok; ++c) {
+            ok = __all_sync(0xffffffffu, ok && wait_empty(im, c));
+            if (!ok) break;
+            if (lane == 0) {
+              if (w == 0) tc::mbar_arrive_expect_tx(&bars->kv_full[s][c], kChunk);
+              else tc::mbar_arrive(&bars->kv_full[s][c]);
             }
-            if (w > 0 || lane > 0) tc::mbar_arrive(&bars->kv_full[s]);
-            im += 1;
-            ++done;
-            if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
-            continue;
+            __syncwarp();
+            if (w == 0 && lane < 2)
+              tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + lane * (kChunk / 2), &p.map, 128 * c, y,
+                              &bars->kv_full[s][c]);
           }
-          // rows from `safe` on are hidden from some of the unit's rows
-          const int safe = max(0, min(32, x.n_all - t.first - 32 * w));
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[r] & ~1ull);
-            if (r < safe || !src)
-              cp_async16(sbase + kVOff + s * kStage + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7),
-                         src ? src + 16 * lane : static_cast<const uint8_t*>(a.main.data), src != nullptr);
-          }
-          for (int r = safe; r < 32; ++r)
-            if (rows[r]) load_rows<1>(rows + r, 32 * w + r, lane, dst, nullptr, mt);
-          asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-          uint8_t* lo = sm + kVOff + (s ^ 1) * kStage;
-#pragma unroll 1
-          for (int r = 0; r < 32; r += 8) load_rows<8>(rows + r, 32 * w + r, lane, dst, lo, mt);
+          for (int k = 0; k < t.images; ++k)
+            for (int c = 0; c < 4; ++c) ok = ok && wait_empty(im + k, c);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float4* mt = meta + slot * kT;
+          uint8_t* dst = sm + kVOff + s * kStage;
+          const uint32_t d0 = sbase + kVOff + s * kStage, d1 = sbase + kVOff + (s ^ 1) * kStage;
+          if (t.images == 1) {
+            // rows from `safe` on are hidden from some of the unit's rows
+            const int safe = max(0, min(32, x.n_all - t.first - 32 * w));
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[32 * w + r]);
+              const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7);
+              if (r < safe || !src)
+                cp_async16(d0 + off, src ? src + 16 * lane : static_cast<const uint8_t*>(a.main.data), src != nullptr);
+            }
+            for (int r = safe; r < 32; ++r) {
+              const uint4* src = reinterpret_cast<const uint4*>(rows[32 * w + r]);
+              if (!src) continue;
+              uint4 v = src[lane];
+              if (__any_sync(0xffffffffu, has_nan_code(v))) {
+                v = make_uint4(0, 0, 0, 0);
+                if (lane == 0) mt[32 * w + r] = item_meta(__int_as_float(0x7fffffff), true);
+              }
+              *reinterpret_cast<uint4*>(dst + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7)) = v;
+            }
+          } else if (!t.entries) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[32 * w + r]);
+              const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7);
+              cp_async16(d0 + off, src ? src + 16 * lane : p.w.raw, src != nullptr);
+              cp_async16(d1 + off, src ? src + kD + 16 * lane : p.w.raw, src != nullptr);
+            }
+          } else {
+            load_bf16_rows(rows + 32 * w, 32 * w, lane, dst, sm + kVOff + (s ^ 1) * kStage, mt);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane < 4)
+            for (int k = 0; k < t.images; ++k) tc::mbar_arrive(&bars->kv_full[(im + k) & 1][lane]);
         }
-        tc::fence_proxy_async_smem();
-        for (int k = 0; k < t.images; ++k) tc::mbar_arrive(&bars->kv_full[(im + k) & 1]);
         im += t.images;
         ++done;
       }
@@ -626,41 +729,69 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     const uint64_t v_k = tc::sw128_desc(sbase + kVOff, 16, 1024), v_m = tc::sw128_desc(sbase + kVOff, 1024, 1024);
     const uint64_t q_k = tc::sw128_desc(sbase + kQOff, 16, 1024);
     const uint64_t p_h = tc::sw128_desc(sbase + kPOff, 1024, 1024), p_l = tc::sw128_desc(sbase + kPOff + 64, 1024, 1024);
-    bool ok = true, seg_open = true;
-    uint32_t im = 0, done = 0, seg = 0;
-    uint32_t filled = 0;  // O^T holds something of this segment
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      const Tile t = tile_of(p, x);
-      const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
-      if (seg_open) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(&bars->q_full, seg & 1, abort_flag));
-        if (!ok) break;
-        seg_open = false;
-        filled = 0;
-      }
-      if (t.count > 0) {
-        for (int k = 0; k < t.images && ok; ++k) {
-          const uint32_t s = (im + k) & 1;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(&bars->kv_full[s], ((im + k) >> 1) & 1, abort_flag));
+    bool ok = true;
+    uint32_t im = 0;  // images before the current tile
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_spin(bar, parity, abort_flag));
+    };
+    // S^T of a tile whose images begin at `m`, 128 dims at a time as they land
+    auto issue_s = [&](uint32_t m, int images) {
+      for (int k = 0; k < images && ok; ++k) {
+        const uint32_t s = (m + k) & 1;
+        const uint64_t vk = v_k + (uint64_t)(s * (kStage >> 4));
+        const uint32_t sfa = tmem + (k ? kLow : kOne);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          wait_all(&bars->kv_full[s][c], ((m + k) >> 1) & 1);
           if (!ok) break;
           tc::tc_fence_after();
           if (leader) {
-            const uint64_t vk = v_k + (uint64_t)(s * (kStage >> 4));
-            const uint32_t sfa = tmem + (k ? kLow : kOne);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_mx(tmem + kSCol, vk + (uint64_t)((c * kChunk + kk * 32) >> 4),
-                       q_k + (uint64_t)((c * kChunk + kk * 32) >> 4), idesc_mx(128, 0, 0), sfa, tmem + kSfQ,
-                       (k | c | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_mx(tmem + kSCol, vk + (uint64_t)((c * kChunk + kk * 32) >> 4),
+                     q_k + (uint64_t)((c * kChunk + kk * 32) >> 4), idesc_mx(128, 0, 0), sfa, tmem + kSfQ,
+                     (k | c | kk) ? 1u : 0u);
           }
           __syncwarp();
         }
+      }
+      if (ok && leader) tc::mma_commit(&bars->s_full);
+      __syncwarp();
+    };
+    // the first tile with items from the walk's position on; `i` its index
+    // among the block's tiles, segments that end without one get their commit
+    int i = 0;
+    uint32_t done = 0, seg = 0;
+    bool opened = false;      // the segment's Q has been waited for
+    bool s_issued = false;    // the current tile's S has been issued
+    uint32_t filled = 0;      // O^T holds something of this segment
+    Tile t = tile_of(p, x);
+    while (i < n_tiles && ok) {
+      const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
+      if (!opened) {
+        wait_all(&bars->q_full, seg & 1);
         if (!ok) break;
-        if (leader) tc::mma_commit(&bars->s_full);
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(&bars->p_full, done & 1, abort_flag));
+        opened = true;
+        filled = 0;
+      }
+      if (t.count > 0 && !s_issued) issue_s(im, t.images);
+      if (seg_last && leader) tc::mma_commit(&bars->q_empty);
+      __syncwarp();
+      // the next tile, while the softmax works on this one
+      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      const Tile nt = i + 1 < n_tiles ? tile_of(p, x) : Tile{false, 0, 0, 0};
+      s_issued = false;
+      if (t.count > 0 && ok) {
+        if (!seg_last && nt.count > 0 && t.images == 1 && nt.images == 1) {
+          // its S too, once the softmax has taken this one's out of tensor memory
+          wait_all(&bars->s_free, done & 1);
+          if (ok) {
+            tc::tc_fence_after();
+            issue_s(im + 1, 1);
+            s_issued = true;
+          }
+        }
+        wait_all(&bars->p_full, done & 1);
         if (!ok) break;
         tc::tc_fence_after();
         if (leader) {
@@ -670,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             const uint64_t vm = v_m + (uint64_t)(s * (kStage >> 4));
             const uint32_t sfa = tmem + (k ? kLow : kOne);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 if (kk < nk) {
@@ -680,8 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
                   mma_mx(tmem + kOCol + kR * c, vm + (uint64_t)((c * kChunk + kk * 4096) >> 4),
                          p_l + (uint64_t)((kk * 4096) >> 4), idesc_mx(64, 1, kk), sfa, tmem + kSfLo, 1u);
                 }
-            tc::mma_commit(&bars->kv_empty[s]);
+              tc::mma_commit(&bars->kv_empty[s][c]);
+            }
           }
+          tc::mma_commit(&bars->p_free);
           tc::mma_commit(&bars->addr_free[done % kRing]);
         }
         __syncwarp();
@@ -693,9 +826,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         if (leader) tc::mma_commit(&bars->pv_done);
         __syncwarp();
         ++seg;
-        seg_open = true;
+        opened = false;
       }
-      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      t = nt;
+      ++i;
     }
     if (!ok && leader) {
       *abort_flag = 1;
@@ -722,9 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     float* red = reinterpret_cast<float*>(sm + kRedOff) + 128 * hh;       // [4][32]
     float* fac = reinterpret_cast<float*>(sm + kFacOff) + 32 * hh;        // [32]
     uint8_t* sf = sm + kSfOff + 128 * hh;                                  // [32][4]
+    volatile int* raise = reinterpret_cast<volatile int*>(sm + kMiscOff + 16) + 2 * hh;
     const uint4* anc = reinterpret_cast<const uint4*>(sm + kAncOff) + 32 * hh + 8 * c4;
     const int4* vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh + 8 * c4;
-    float2* my_ar = row_ar + 32 * hh + 8 * c4;
     if (hh == 0) {
       const uint32_t one = 0x7f7f7f7fu, low = 0x7b7b7b7bu;
       tmem_st4(lanes + kOne, one, one, one, one);
@@ -738,75 +872,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     int seg_tile0 = 0;
     uint32_t done = 0, seg = 0;
     float l[8], fa[8], ref[8];
+    if (w == 0 && lane < 2) raise[lane] = 0;
     for (int i = 0; i < n_tiles; ++i) {
       if (seg_open) {
-        // the unit's Q, the rows' factors, references and masks. Every product
-        // that reads the last unit's Q has completed (its S was read), and both
-        // halves are done with its place.
-        if (seg > 0) {
-          ok = tc::mbar_wait(&bars->epi, (seg - 1) & 1, abort_flag);
-          if (named_or(bar, !ok)) {
-            ok = false;
-            break;
-          }
-        }
+        // the rows' factors, references and masks
         seg_open = false;
         any = false;
         seg_tile0 = x.tile;
-        auto put_q = [&](int k, uint4 hi, uint4 lo, uint32_t m) {
-          const int n = 8 * w + k;                                    // row of the half
-          const int at = 32 * hh + 8 * (k >> 1) + 2 * w + (k & 1);    // row of Q
-          uint8_t* dst = sm + kQOff + (lane >> 3) * kChunk;
-          *reinterpret_cast<uint4*>(dst + tc::sw128_off(at, lane & 7)) = hi;
-          *reinterpret_cast<uint4*>(dst + tc::sw128_off(kR + at, lane & 7)) = lo;
-          if (lane == 0)
-            row_ar[32 * hh + n] = make_float2(m >= 0x7f800000u ? __int_as_float(0x7fffffff)
-                                                               : scale_down(m) * (a.sm_scale * 1.4426950408889634f),
-                                              kNone);
-        };
-        const int n0 = 32 * hh + 8 * w;
-        const size_t q_at = (size_t)(x.row0 + n0) * kD + 16 * lane;
-        if (a.q_dtype == V4KV_FP32) {
-#pragma unroll 1
-          for (int k0 = 0; k0 < 8; k0 += 2) {
-            float4 f[2][4];
+        const float* qf = p.w.q_factor + (size_t)q_image(p, x.q, x.b, x.u) * kR + 32 * hh + 8 * c4;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                f[k][e] = n0 + k0 + k < x.nrows
-                              ? reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + q_at + (size_t)(k0 + k) * kD)[e]
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float* v = reinterpret_cast<const float*>(f[k]);
-              uint32_t m = 0;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-              m = __reduce_max_sync(0xffffffffu, m);
-              uint4 hi, lo;
-              split16(v, scale_up(m), hi, lo);
-              put_q(k0 + k, hi, lo, m);
-            }
-          }
-        } else {
-          uint4 raw[8][2];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              raw[k][e] = n0 + k < x.nrows
-                              ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + (size_t)k * kD)[e]
-                              : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t m = amax_bf16(raw[k]);
-            float v[16];
-            bf16x16(raw[k], v);
-            uint4 hi, lo;
-            split16(v, scale_up(m), hi, lo);
-            put_q(k, hi, lo, m);
-          }
+        for (int m = 0; m < 8; ++m) {
+          l[m] = 0.f;
+          fa[m] = qf[m];
+          ref[m] = kNone;
         }
         if (w == 0) {
           const int n = 32 * hh + lane;
@@ -815,28 +893,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           node += x.q.s.first;
           const int w0 = max(0, x.q.L + p.w.depth[node] + 1 - a.window_len);
           reinterpret_cast<uint4*>(sm + kAncOff)[n] = p.w.anc[node];
-          reinterpret_cast<int4*>(sm + kVisOff)[n] = make_int4(w0 / a.ratio, w0, node, 0);
+          reinterpret_cast<int4*>(sm + kVisOff)[n] = make_int4(w0 >> p.ratio_log, w0, node, 0);
+          row_ref[n] = kNone;
         }
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        tc::mbar_arrive(&bars->q_full);
         named_sync(bar);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          l[m] = 0.f;
-          fa[m] = my_ar[m].x;
-          ref[m] = kNone;
-        }
       }
       const Tile t = tile_of(p, x);
       const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
       if (t.count > 0) {
         ok = tc::mbar_wait_spin(&bars->s_full, done & 1, abort_flag, 32);
         tc::tc_fence_after();
-        // scores times the items' scales: s[j][m]
-        float s[4][8], ks[4];
+        // the items' {scale, log2 |scale|, 1 / |scale|} and the scores u[j][m],
+        // log2 of a weight of the item's codes
+        float u[4][8], inv[4];
         uint32_t seen = 0;  // bit 8 j + m: row m sees item j
-        auto load_s = [&]() {
+        bool plain = true;  // all scales positive
+        {
+          float ks[4], lg[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 mt = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j];
+            ks[j] = mt.x;
+            lg[j] = mt.y;
+            inv[j] = mt.z;
+            seen |= (mt.w == 0.f ? 0xffu : 0u) << (8 * j);
+            plain &= mt.x > 0.f;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t h[16], q[16];
@@ -848,17 +930,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
 #pragma unroll
               for (int m = 0; m < 8; ++m) {
                 const int r = 4 * (m >> 1) + 2 * j + (m & 1);
-                s[2 * k + j][m] = (__uint_as_float(h[r]) + __uint_as_float(q[r])) * ks[2 * k + j];
+                u[2 * k + j][m] =
+                    fmaf((__uint_as_float(h[r]) + __uint_as_float(q[r])) * ks[2 * k + j], fa[m], lg[2 * k + j]);
               }
           }
-        };
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 mt = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j];
-          ks[j] = mt.x;
-          seen |= (mt.y == 0.f ? 0xffu : 0u) << (8 * j);
         }
-        load_s();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->s_free);
         if (!p.per_node && (!t.entries || t.first + kT > x.n_all)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -878,50 +957,93 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             }
           }
         }
-        // exponents relative to the rows' references (a weight is 2^s)
-        float extra = 0.f;  // a large scale counts in a weight's size
-#pragma unroll
-        for (int j = 0; j < 4; ++j) extra = fmaxf(extra, fabsf(ks[j]));
-        extra = extra > 1.f ? __log2f(extra) : 0.f;
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int m = 0; m < 8; ++m) s[j][m] = fmaf(s[j][m], fa[m], -ref[m]);
         if (seen != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int m = 0; m < 8; ++m)
-              if (!(seen >> (8 * j + m) & 1)) s[j][m] = -INFINITY;
+              if (!(seen >> (8 * j + m) & 1)) u[j][m] = -INFINITY;
         }
+        // Per row, the exponent ex that puts the warp's 32 weights below 2^8,
+        // the largest in [2^7, 2^8): a weight is u = 2^ex times what is stored.
+        float ex[8], lt[8];
+        bool high = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < 8; ++m) {
+          float mx = fmaxf(fmaxf(u[0][m], u[1][m]), fmaxf(u[2][m], u[3][m]));
 #pragma unroll
-          for (int m = 0; m < 8; ++m) top = fmaxf(top, s[j][m]);
-        if (named_or(bar, top + extra > kRaise || !ok)) {
-          if (named_or(bar, !ok)) {
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          ex[m] = mx == -INFINITY ? -INFINITY : floorf(mx) - 7.f;
+          high |= ex[m] > ref[m] + kRaise;
+          const float c = mx == -INFINITY ? 0.f : ex[m];
+          lt[m] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            u[j][m] = fast_exp2(u[j][m] - c);
+            lt[m] = fmaf(u[j][m], inv[j], lt[m]);
+          }
+        }
+        if (__any_sync(0xffffffffu, !plain)) {
+          // signs, and items of no value
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float ks = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j].x;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+              u[j][m] = ks == 0.f ? 0.f : ks < 0.f ? -u[j][m] : u[j][m];
+          }
+        }
+        if (__any_sync(0xffffffffu, high) && lane == 0) raise[done & 1] = 1;
+        // the last tile's product has read P and its scales
+        if (done > 0) ok = ok && tc::mbar_wait(&bars->p_free, (done - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) {
+          *abort_flag = 1;
+          raise[done & 1] = 2;
+        }
+        const uint32_t pcol = 2 * hh + (c4 >> 1), pbyte = 8 * (c4 & 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hw[2], lw[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t h0, h1, l0, l1;
+            split2(u[j][4 * q], u[j][4 * q + 1], h0, l0);
+            split2(u[j][4 * q + 2], u[j][4 * q + 3], h1, l1);
+            hw[q] = h0 | (h1 << 16);
+            lw[q] = l0 | (l1 << 16);
+          }
+          const int item = 32 * w + (lane >> 2) + 8 * j;
+          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, pcol) + pbyte) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, 4 + pcol) + pbyte) = make_uint2(lw[0], lw[1]);
+        }
+        // The block scales 2^(ex - ref), a byte per row and warp: lane
+        // (lane / 4, c) writes row 8 c + lane / 4.
+        auto put_scales = [&]() {
+          float e = ex[0], r = ref[0];
+#pragma unroll
+          for (int m = 1; m < 8; ++m)
+            if (lane >> 2 == m) {
+              e = ex[m];
+              r = ref[m];
+            }
+          const float d = e == -INFINITY ? -122.f : fminf(fmaxf(e - r, -122.f), 120.f);
+          sf[4 * (8 * c4 + (lane >> 2)) + w] = (uint8_t)((int)d + 127);
+        };
+        put_scales();
+        named_sync(bar);
+        const int up = raise[done & 1];
+        if (up) {
+          if (up == 2) {  // a wait gave up: the four warps leave together
             ok = false;
             break;
           }
-          // raise the references to the rows' maxima so far, O^T and the sums
-          // with them (the scores are taken from S again: a reference of kNone
-          // has swallowed them)
-          load_s();
+          // a row's weights passed its reference by 2^kRaise: raise it, and
+          // O^T (the product before this tile is done), sums and scales with it
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              s[j][m] = (seen >> (8 * j + m) & 1) ? s[j][m] * fa[m] : -INFINITY;
-              mx = fmaxf(mx, s[j][m]);
-            }
-            mx += extra;
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane < 4) red[32 * w + 8 * c4 + m] = mx;
-          }
+          for (int m = 0; m < 8; ++m)
+            if (lane < 4) red[32 * w + 8 * c4 + m] = ex[m];
           named_sync(bar);
+          if (w == 0 && lane == 0) raise[done & 1] = 0;
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const int n = 8 * c4 + m;
@@ -931,14 +1053,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             l[m] *= f;
             if (w == 0 && lane < 4) {
               fac[n] = f;
-              my_ar[m].y = nm;
+              row_ref[32 * hh + n] = nm;
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j][m] -= nm;
           }
+          put_scales();
           named_sync(bar);
           if (any) {
-            // S is complete, so the last tile's product into O^T is
 #pragma unroll 1
             for (int g = 0; g < 16; ++g) {
               const uint32_t at = lanes + kOCol + kR * (g >> 2) + 32 * hh + 8 * (g & 3);
@@ -953,66 +1073,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           }
         }
         any = true;
-        // weights of the items' codes
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const float pr = fast_exp2(s[j][m]);
-            l[m] += pr;
-            s[j][m] = pr * ks[j];
-          }
-        if (seen != 0xffffffffu) {  // 0 * NaN
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-              if (!(seen >> (8 * j + m) & 1)) s[j][m] = 0.f;
+        for (int m = 0; m < 8; ++m) {
+          // 2^(ex - ref), an integer power below 2^41
+          const float d = fmaxf(ex[m] - ref[m], -127.f);
+          l[m] = fmaf(lt[m], __int_as_float(((int)d + 127) << 23), l[m]);
         }
-        // largest magnitude of the 32 items per row: the upper halves of two
-        // rows' bits in a word (the exponent and seven bits, which order alike)
-        uint32_t bytes[2] = {0, 0};
-        float mul[8];
-#pragma unroll
-        for (int m = 0; m < 8; m += 2) {
-          uint32_t e = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            e = __vmaxu2(e, __byte_perm(__float_as_uint(s[j][m]), __float_as_uint(s[j][m + 1]), 0x7632) & 0x7fff7fffu);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) e = __vmaxu2(e, __shfl_xor_sync(0xffffffffu, e, o));
-          const uint32_t b0 = max((e & 0xffffu) >> 7, 16u), b1 = max(e >> 23, 16u);
-          // into [2^7, 2^8), and the block scale's byte that undoes it
-          mul[m] = __uint_as_float((261u - b0) << 23);
-          mul[m + 1] = __uint_as_float((261u - b1) << 23);
-          bytes[m >> 2] |= ((b0 - 7u) | ((b1 - 7u) << 8)) << (16 * ((m >> 1) & 1));
-        }
-        sf[4 * (8 * c4 + (lane >> 2)) + w] = (uint8_t)((lane & 16 ? bytes[1] : bytes[0]) >> (8 * ((lane >> 2) & 3)));
-        // the two terms of four items, eight rows each
-        const uint32_t pcol = 2 * hh + (c4 >> 1), pbyte = 8 * (c4 & 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t hw[2], lw[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t h0, h1, l0, l1;
-            split2(s[j][4 * q] * mul[4 * q], s[j][4 * q + 1] * mul[4 * q + 1], h0, l0);
-            split2(s[j][4 * q + 2] * mul[4 * q + 2], s[j][4 * q + 3] * mul[4 * q + 3], h1, l1);
-            hw[q] = h0 | (h1 << 16);
-            lw[q] = l0 | (l1 << 16);
-          }
-          const int item = 32 * w + (lane >> 2) + 8 * j;
-          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, pcol) + pbyte) = make_uint2(hw[0], hw[1]);
-          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, 4 + pcol) + pbyte) = make_uint2(lw[0], lw[1]);
-        }
-        named_sync(bar);
         const uint32_t word = reinterpret_cast<const uint32_t*>(sf)[lane];
         tmem_st1(lanes + kSfHi + hh, word);
         tmem_st1(lanes + kSfLo + hh, word - 0x04040404u);
         tc::tmem_wait_st();
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
-        tc::mbar_arrive(&bars->p_full);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full);
         ++done;
       }
       if (seg_last) {
@@ -1038,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         if (w == 0) {
           const float sum = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
           fac[lane] = whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;  // a NaN stays one
-          if (!whole) p.w.part_ml[slot * kR + 32 * hh + lane] = make_float2(row_ar[32 * hh + lane].y, sum);
+          if (!whole) p.w.part_ml[slot * kR + 32 * hh + lane] = make_float2(row_ref[32 * hh + lane], sum);
         }
         named_sync(bar);
         // O^T: lane = dim 128 c + 32 w + lane, column = row
@@ -1054,70 +1128,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
               if (32 * hh + n < x.nrows) o[n * kD] = any ? __uint_as_float(r32[n]) : 0.f;
           }
         } else {
-          // rows of bf16 in Q's place (its products are done), half hh's 32 KB
-          // of it, then one copy of the rows, which are consecutive in `out`
-          uint8_t* stage = sm + kQOff + 32768 * hh;
           const int4* row_vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh;
+          const int pairs = a.rope.rope_dim >> 1;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const int d = 128 * c + 32 * w + lane, pair = (d - a.rope.rope_offset) >> 1;
-            const bool rot = d >= a.rope.rope_offset && d < a.rope.rope_offset + a.rope.rope_dim;
-            const bool any_rot = __any_sync(0xffffffffu, rot);
-#pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-              uint32_t r8[8];
-              float v[8];
-              tmem_ld8(lanes + kOCol + kR * c + 32 * hh + 8 * g, r8);
-              tc::tmem_wait_ld();
+          for (int g = 0; g < 16; ++g) {
+            const int d = 128 * (g >> 2) + 32 * w + lane, pair = (d - a.rope.rope_offset) >> 1;
+            const bool rot = d >= a.rope.rope_offset && pair < pairs;
+            const int r0 = 8 * (g & 3);
+            uint32_t r8[8];
+            float v[8];
+            tmem_ld8(lanes + kOCol + kR * (g >> 2) + 32 * hh + r0, r8);
+            tc::tmem_wait_ld();
 #pragma unroll
-              for (int n = 0; n < 8; ++n) v[n] = any ? __uint_as_float(r8[n]) * fac[8 * g + n] : 0.f;
-              if (any_rot) {
-                float cs = 1.f, sn = 0.f;
-                int have = -1;
+            for (int n = 0; n < 8; ++n) v[n] = any ? __uint_as_float(r8[n]) * fac[r0 + n] : 0.f;
+            if (__any_sync(0xffffffffu, rot)) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                  const float other = __shfl_xor_sync(0xffffffffu, v[n], 1);
-                  const int node = row_vis[8 * g + n].z;
-                  if (rot) {
-                    if (node != have) {
-                      have = node;
-                      if (pair < kPairs) {
-                        const float2 f = p.w.rope[(size_t)node * kPairs + pair];
-                        cs = f.x;
-                        sn = f.y;
-                      } else {
-                        rope_cs(a.rope, pair, (long long)x.q.L + p.w.depth[node], &cs, &sn);
-                      }
-                    }
-                    v[n] = (d & 1) ? __fadd_rn(__fmul_rn(other, -sn), __fmul_rn(v[n], cs))
-                                   : __fsub_rn(__fmul_rn(v[n], cs), __fmul_rn(other, -sn));
-                  }
+              for (int n = 0; n < 8; ++n) {
+                const float other = __shfl_xor_sync(0xffffffffu, v[n], 1);
+                if (rot) {
+                  const float2 f = p.w.rope[(size_t)row_vis[r0 + n].z * pairs + pair];
+                  v[n] = (d & 1) ? __fadd_rn(__fmul_rn(other, -f.y), __fmul_rn(v[n], f.x))
+                                 : __fsub_rn(__fmul_rn(v[n], f.x), __fmul_rn(other, -f.y));
                 }
               }
-              // even lanes store a pair of dims of rows 2 k, odd lanes of rows 2 k + 1
+            }
+            // even lanes store a pair of dims of rows r0 + 2 k, odd lanes of the row after
+            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (size_t)(x.row0 + 32 * hh + r0 + (lane & 1)) * kD + (d & ~1));
 #pragma unroll
-              for (int n = 0; n < 8; n += 2) {
-                const float give = lane & 1 ? v[n] : v[n + 1];
-                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-                const uint32_t w2 = lane & 1 ? float_to_bf16_bits(got) | ((uint32_t)float_to_bf16_bits(v[n + 1]) << 16)
-                                             : float_to_bf16_bits(v[n]) | ((uint32_t)float_to_bf16_bits(got) << 16);
-                *reinterpret_cast<uint32_t*>(stage + (8 * g + n + (lane & 1)) * (2 * kD) + 2 * (d & ~1)) = w2;
-              }
+            for (int n = 0; n < 8; n += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v[n] : v[n + 1], 1);
+              const float first = lane & 1 ? got : v[n], second = lane & 1 ? v[n + 1] : got;
+              if (32 * hh + r0 + n + (lane & 1) < x.nrows)
+                o[n * (kD / 2)] = float_to_bf16_bits(first) | ((uint32_t)float_to_bf16_bits(second) << 16);
             }
           }
-          tc::fence_proxy_async_smem();
-          named_sync(bar);
-          const int rows = min(32, x.nrows - 32 * hh);
-          if (w == 0 && lane == 0 && rows > 0) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                             a.out + (size_t)(x.row0 + 32 * hh) * kD),
-                         "r"(sbase + kQOff + 32768 * hh), "r"(rows * 2 * kD)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          }
         }
-        if (w == 0 && lane == 0) tc::mbar_arrive(&bars->epi);
         named_sync(bar);  // fac and the references are free
         seg_open = true;
       }
@@ -1188,15 +1233,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     for (int e = 0; e < 4; e += 2) {
       const int d = 128 * q + 4 * lane + e - a.rope.rope_offset;
       if (d >= 0 && d < a.rope.rope_dim) {
-        float cs, sn;
-        if ((d >> 1) < kPairs) {
-          const float2 f = p.w.rope[(size_t)node * kPairs + (d >> 1)];
-          cs = f.x;
-          sn = f.y;
-        } else {
-          rope_cs(a.rope, d >> 1, (long long)x.q.L + p.w.depth[node], &cs, &sn);
-        }
-        rope_apply(v[e], v[e + 1], cs, -sn);
+        const float2 f = p.w.rope[(size_t)node * (a.rope.rope_dim >> 1) + (d >> 1)];
+        rope_apply(v[e], v[e + 1], f.x, -f.y);
       }
     }
     const uint32_t lo = float_to_bf16_bits(v[0]) | ((uint32_t)float_to_bf16_bits(v[1]) << 16);
@@ -1205,8 +1243,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   }
 }
 
-// grid (batch + 1). Block b < batch: depths, ancestors and rotations of its
-// sequence's nodes. Block `batch`: the sequences' costs and the blocks' ranges.
+// Blocks b < batch: depths, ancestors and rotations of a sequence's nodes. Block
+// `batch`: the sequences' costs and the blocks' ranges. The others: raw rows (a
+// warp takes kPrepRows of a sequence) as two e4m3 terms, once for all units.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ Params p) {
   tc::pdl_wait();
   tc::pdl_launch_dependents();
@@ -1233,13 +1272,130 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       depth[t] = d;
     }
     __syncthreads();
-    const int L = seq_len(a, b), pairs = min(kPairs, a.rope.rope_dim / 2);
-    if (lane < pairs)
-      for (int i = warp; i < s.n; i += 8) {
-        float c, sn;
-        rope_cs(a.rope, lane, (long long)L + depth[i], &c, &sn);
-        p.w.rope[(size_t)(s.first + i) * kPairs + lane] = make_float2(c, sn);
+    const int L = seq_len(a, b), pairs = a.rope.rope_dim >> 1;
+    for (int k = t; k < s.n * pairs; k += 256) {
+      const int i = k / pairs;
+      float c, sn;
+      rope_cs(a.rope, k - i * pairs, (long long)L + depth[i], &c, &sn);
+      p.w.rope[(size_t)s.first * pairs + k] = make_float2(c, sn);
+    }
+    return;
+  }
+  const int raw_end = a.batch + 1 + a.batch * p.raw_blocks;
+  if (b >= raw_end) {
+    // half a unit's Q: row 8 c + 2 k + e of a half at row 8 k + 2 c + e of the
+    // half (hi terms) and 64 rows on (lo terms)
+    const int g = (b - raw_end) >> 1, hh = (b - raw_end) & 1;
+    const int bb = g / p.max_units, uu = g - bb * p.max_units;
+    const SeqPlan q = plan_of(p, bb, nullptr);
+    if (uu >= q.units) return;
+    int nrows;
+    size_t row0;
+    if (p.per_node) {
+      const int i = uu / p.hc, h0 = (uu - i * p.hc) * kR;
+      nrows = min(kR, a.heads - h0);
+      row0 = (size_t)(q.s.first + i) * a.heads + h0;
+    } else {
+      nrows = min(kR, q.s.n * a.heads - uu * kR);
+      row0 = (size_t)q.s.first * a.heads + uu * kR;
+    }
+    const int img = q_image(p, q, bb, uu);
+    uint4 raw[kPrepRows][4];
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) {
+      const int n = 32 * hh + kPrepRows * warp + k;
+      const size_t at = (row0 + n) * kD + 16 * lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        raw[k][e] = make_uint4(0, 0, 0, 0);
+        if (n >= nrows) continue;
+        if (a.q_dtype == V4KV_FP32) raw[k][e] = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at)[e];
+        else if (e < 2) raw[k][e] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at)[e];
       }
+    }
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) {
+      float v[16];
+      if (a.q_dtype == V4KV_FP32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[4 * e] = __uint_as_float(raw[k][e].x);
+          v[4 * e + 1] = __uint_as_float(raw[k][e].y);
+          v[4 * e + 2] = __uint_as_float(raw[k][e].z);
+          v[4 * e + 3] = __uint_as_float(raw[k][e].w);
+        }
+      } else {
+        bf16x16(raw[k], v);
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+      m = __reduce_max_sync(0xffffffffu, m);
+      uint4 hi, lo;
+      split16(v, scale_up(m), hi, lo);
+      const int n = kPrepRows * warp + k;  // row of the half: 8 c + 2 k + e
+      const int at = 32 * hh + 8 * ((n >> 1) & 3) + 2 * (n >> 3) + (n & 1);
+      uint8_t* dst = p.w.q + (size_t)img * 65536 + (lane >> 3) * kChunk;
+      *reinterpret_cast<uint4*>(dst + tc::sw128_off(at, lane & 7)) = hi;
+      *reinterpret_cast<uint4*>(dst + tc::sw128_off(kR + at, lane & 7)) = lo;
+      if (lane == 0)
+        p.w.q_factor[(size_t)img * kR + 32 * hh + n] =
+            m >= 0x7f800000u ? __int_as_float(0x7fffffff) : scale_down(m) * (a.sm_scale * 1.4426950408889634f);
+    }
+    return;
+  }
+  if (b > a.batch) {
+    const int per = p.raw_blocks, bb = (b - a.batch - 1) / per;
+    const SeqPlan q = plan_of(p, bb, nullptr);
+    const int w0 = raw_w0(a, q), n_win = q.L - w0, n = q.s.n > 0 ? n_win + q.s.n : 0;
+    const int r0 = ((b - a.batch - 1) % per * 8 + warp) * kPrepRows;
+    const bool fp8 = a.window.dtype == V4KV_FP8_E4M3;
+    const size_t base = raw_row0(a, q, bb);
+    uint4 raw[kPrepRows][2];
+    float scale[kPrepRows];
+    int kind[kPrepRows];  // 0: no such row, 1: bf16, 2: fp8
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) {
+      raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
+      scale[k] = 0.f;
+      kind[k] = 0;
+      const int r = r0 + k;
+      if (r >= n) continue;
+      const uint4* src = nullptr;
+      if (r >= n_win) {
+        src = reinterpret_cast<const uint4*>(a.k_tree + (size_t)(q.s.first + r - n_win) * kD);
+        kind[k] = 1;
+      } else {
+        const int tok = w0 + r;
+        const int pg = page_of(a.window.block_table + (size_t)bb * a.window.max_blocks, a.window.max_blocks, tok,
+                               a.window.spb, a.window.num_pages, a.dev_status);
+        if (pg < 0) continue;
+        const size_t slot = (size_t)pg * a.window.spb + tok % a.window.spb;
+        kind[k] = fp8 ? 2 : 1;
+        src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.window.data) + slot * (fp8 ? kD : 2 * kD));
+        if (fp8) scale[k] = a.window.scales[slot];
+      }
+      raw[k][0] = src[kind[k] == 2 ? lane : 2 * lane];
+      if (kind[k] == 1) raw[k][1] = src[2 * lane + 1];
+    }
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) {
+      if (kind[k] == 0) {
+        if (r0 + k < n && lane == 0) p.w.raw_meta[base + r0 + k] = make_float2(0.f, -INFINITY);
+        continue;
+      }
+      uint4 hi = raw[k][0], lo = make_uint4(0, 0, 0, 0);
+      if (kind[k] == 1) {
+        scale[k] = split_row(raw[k], hi, lo);
+      } else if (__any_sync(0xffffffffu, has_nan_code(hi))) {
+        hi = lo;
+        scale[k] = __int_as_float(0x7fffffff);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.w.raw + (base + r0 + k) * (2 * kD));
+      dst[lane] = hi;
+      dst[32 + lane] = lo;
+      if (lane == 0) p.w.raw_meta[base + r0 + k] = make_float2(scale[k], 0.f);
+    }
     return;
   }
   __shared__ long long csum[8];
@@ -1285,10 +1441,11 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     }
     __syncthreads();
   }
+  const int blocks = min(p.grid, tcarry);
   for (int c = t; c <= p.grid; c += 256) {
     int4 rec = make_int4(tcarry, a.batch, 0, 0);
-    if (c < p.grid && ccarry > 0) {
-      const long long target = (long long)c * ccarry / p.grid;
+    if (c < blocks) {
+      const long long target = (long long)c * ccarry / blocks;
       int lo = 0, hi = a.batch - 1;  // the last sequence that begins at or before the target
       while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
@@ -1308,7 +1465,8 @@ namespace {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-size_t layout(TreeWs* w, uint8_t* base, int batch, int total_nodes, int grid) {
+size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, int k, int window_len,
+              int max_len, int grid) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = base ? base + at : nullptr;
@@ -1319,6 +1477,14 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int total_nodes, int grid) {
   x.anc = reinterpret_cast<uint4*>(take((size_t)total_nodes * sizeof(uint4)));
   x.depth = reinterpret_cast<int32_t*>(take((size_t)total_nodes * 4));
   x.rope = reinterpret_cast<float2*>(take((size_t)total_nodes * kPairs * sizeof(float2)));
+  // q_image() at most: whole units per node, or rows in units and one per sequence
+  const size_t images = heads % kR == 0 || k > 0 ? (size_t)total_nodes * ((heads + kR - 1) / kR)
+                                                 : (size_t)total_nodes * heads / kR + batch + 1;
+  x.q = take(images * 65536);
+  x.q_factor = reinterpret_cast<float*>(take(images * kR * sizeof(float)));
+  const size_t raws = (size_t)batch * (window_len - 1 < max_len ? window_len - 1 : max_len) + total_nodes;
+  x.raw = take(raws * 2 * kD);
+  x.raw_meta = reinterpret_cast<float2*>(take(raws * sizeof(float2)));
   x.cost = reinterpret_cast<long long*>(take(((size_t)batch + 1) * 8));
   x.tiles = reinterpret_cast<int32_t*>(take(((size_t)batch + 1) * 4));
   x.rec = reinterpret_cast<int4*>(take(((size_t)grid + 1) * sizeof(int4)));
@@ -1330,8 +1496,9 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int total_nodes, int grid) {
 
 }  // namespace
 
-size_t tree_workspace_bytes(int batch, int, int total_nodes, int, int num_sms) {
-  return layout(nullptr, nullptr, batch, total_nodes, num_sms);
+size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int k, int window_len, int max_len,
+                            int num_sms) {
+  return layout(nullptr, nullptr, batch, heads, total_nodes, k, window_len, max_len, num_sms);
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream) {
@@ -1340,7 +1507,12 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   p.grid = num_sms;
   p.per_node = a.topk != nullptr || a.heads % kR == 0;
   p.hc = (a.heads + kR - 1) / kR;
-  layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.total_nodes, p.grid);
+  p.max_units = p.per_node ? a.max_nodes * p.hc : (a.max_nodes * a.heads + kR - 1) / kR;
+  p.ratio_log = a.ratio == 4 ? 2 : 7;
+  p.spb_log = 8 - p.ratio_log;
+  p.raw_blocks = (min(a.window_len - 1, a.max_len) + a.max_nodes + 8 * kPrepRows - 1) / (8 * kPrepRows);
+  layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.heads, a.total_nodes, a.topk ? a.k : 0, a.window_len,
+         a.max_len, p.grid);
   cudaError_t e = cudaSuccess;
   p.pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64;
   if (p.pages) {
@@ -1350,7 +1522,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1), dim3(256), 0, stream, p);
+  e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1 + a.batch * (p.raw_blocks + 2 * p.max_units)), dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_attend_kernel, dim3(p.grid), dim3(kThreads), kSmemBytes, stream, p);
   if (e != cudaSuccess) return e;
