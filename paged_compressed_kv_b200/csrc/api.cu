@@ -420,6 +420,8 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
                                 int32_t* dev_status, void* stream) {
   if (!tree_ok(batch, cu_nodes, total_nodes, max_nodes)) return V4KV_ERR_INVALID_ARG;
   if (total_nodes > 0 && (!parents || !k_tree || !aligned16(k_tree))) return V4KV_ERR_INVALID_ARG;
+  if ((long long)total_nodes * heads > 0x7fffffffLL || (long long)batch * window_len + total_nodes > 0x7fffffffLL)
+    return V4KV_ERR_UNSUPPORTED;
   // no drafted token may leave the window: the entries it would belong to do not exist
   if (window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
   // the other arguments are checked as v4kv_decode_attention checks them (the

@@ -30,9 +30,9 @@
 // The normaliser and the running reference are fp32. With block scales P needs
 // no fixed range, so the reference moves only when a score passes it by 2^40.
 //
-// Warps: 0-7 softmax (a thread has 4 items of the tile and 8 of the rows) and
-// the unit's epilogue, 8-11 load tiles, 12 issues the MMAs, 13 and 14 resolve
-// the even and odd tiles' row addresses ahead, 15 loads the units' Q. The prep
+// Warps: 0-15 softmax (a thread has 4 items of the tile and 4 of the rows) and
+// the unit's epilogue, 16-19 load tiles, 20 issues the MMAs, 21 and 22 resolve
+// the even and odd tiles' row addresses ahead, 23 loads the units' Q. The prep
 // kernel has written every Q as the image its products read, and every raw row
 // as its two terms, once for all units that use it.
 //
@@ -51,7 +51,7 @@ namespace {
 constexpr int kR = 64;    // rows of a unit
 constexpr int kT = 128;   // items of a tile
 constexpr int kD = 512;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kRing = 4;  // tiles whose rows are resolved ahead
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr float kRaise = 40.f;   // log2 by which a score may pass its reference
@@ -69,11 +69,11 @@ constexpr uint32_t kPtrOff = kMetaOff + kRing * 2048;  // [kRing][128] row addre
 constexpr uint32_t kRowOff = kPtrOff + kRing * 1024; // [64] the rows' references
 constexpr uint32_t kAncOff = kRowOff + 512;   // [64] ancestors of the row's node, 128 bits
 constexpr uint32_t kVisOff = kAncOff + 1024;  // [64] {visible entries, first visible token, node}
-constexpr uint32_t kRedOff = kVisOff + 1024;   // [8][32] reductions over a warp's items
+constexpr uint32_t kRedOff = kVisOff + 1024;  // [2][4][32] reductions over a warp's items
 constexpr uint32_t kSfOff = kRedOff + 1024;   // [64] block scales of P, a byte per 32 items
 constexpr uint32_t kFacOff = kSfOff + 256;    // [64] per-row factors
 constexpr uint32_t kBarOff = kFacOff + 256;
-constexpr uint32_t kMiscOff = kBarOff + 256;
+constexpr uint32_t kMiscOff = kBarOff + 320;
 constexpr uint32_t kSmemBytes = kMiscOff + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
@@ -90,9 +90,9 @@ constexpr uint32_t kCols = 512;
 struct Bars {
   uint64_t kv_full[2][4], kv_empty[2][4];  // per stage and 128 dims
   uint64_t addr_full[kRing], addr_free[kRing];
-  uint64_t q_full, q_empty, s_full, s_free, p_full, p_free, pv_done, drain;
+  uint64_t ready, q_full, q_empty, s_full, s_free, p_full, p_free, pv_done, drain;
 };
-static_assert(sizeof(Bars) <= 256, "barrier area");
+static_assert(sizeof(Bars) <= 320, "barrier area");
 
 // What the prep kernel leaves in the workspace.
 struct TreeWs {
@@ -101,11 +101,12 @@ struct TreeWs {
   float2* rope;       // [total_nodes][rope_dim / 2] cos, sin at the node's position
   uint8_t* q;         // the units' Q as shared-memory images, 64 KB each
   float* q_factor;    // their rows' score factors, 64 each
+  int4* units;        // [images][4] Unit's fields
   uint8_t* raw;       // rows of the windows and trees as two e4m3 terms, 512 bytes each
   float2* raw_meta;   // their {scale, 0 or -inf: no such row}
   long long* cost;    // [batch + 1] prefix sums over sequences
   int32_t* tiles;     // [batch + 1]
-  int4* rec;          // [grid + 1] a block's first tile: {index, sequence, unit in it, tile in that}
+  int4* rec;          // [grid + 1] a block's first tile: {index, its unit, -, tile in that}
   float* part_o;      // [2 grid][64][512]
   float2* part_ml;    // [2 grid][64]
 };
@@ -142,9 +143,9 @@ __device__ __forceinline__ int raw_w0(const TreeArgs& a, const SeqPlan& q) {
   return min(q.L, max(0, q.L + 1 - a.window_len));
 }
 
-// Index of a unit's Q image. Distinct: a sequence's units are at most one more
-// than its rows fill.
-__device__ __forceinline__ int q_image(const Params& p, const SeqPlan& q, int b, int u) {
+// A unit's index, of its Q image and its fields: consecutive within a sequence
+// and distinct, as a sequence's units are at most one more than its rows fill.
+__device__ __forceinline__ int unit_index(const Params& p, const SeqPlan& q, int b, int u) {
   return p.per_node ? q.s.first * p.hc + u : b + (int)((long long)q.s.first * p.a.heads / kR) + u;
 }
 
@@ -178,61 +179,67 @@ __device__ __forceinline__ int tile_at_cost(const Params& p, const SeqPlan& q, i
 
 // A unit: its rows, and the items its tiles hold.
 struct Unit {
-  int b, u, tile;      // the walk's position
-  SeqPlan q;
-  int node0;           // first node
-  int nrows;
-  long long row0;      // first row of out and q
-  int n_ent;           // entries in the list (top-k slots, or visible to the deepest row)
-  int n_all;           // entries that every row sees
+  int g, tile;         // index, the walk's position in it
+  int row0, nrows;     // rows of q and out
+  int te, tr;          // tiles of entries, of raw rows
+  int n_ent, n_all;    // entries in the list (top-k slots, or those that the deepest row sees); seen by every row
   int w0, n_win;       // first cached token in the list, and how many
   int n_tree;          // nodes in the list
+  int node0, first;    // its first node, and the sequence's
+  int L, b;
+  int raw, raw_tree;   // the raw rows of the list's first token and of the sequence's first node
+  int next;            // next unit's index, -1 behind the last
 };
 
-__device__ __forceinline__ void unit_set(const Params& p, Unit& x) {
-  const TreeArgs& a = p.a;
-  const int L = x.q.L, W = a.window_len;
-  if (p.per_node) {
-    const int i = x.u / p.hc, h0 = (x.u % p.hc) * kR;
-    x.node0 = i;
-    x.nrows = min(kR, a.heads - h0);
-    x.row0 = (long long)(x.q.s.first + i) * a.heads + h0;
-    const int d = p.w.depth[x.q.s.first + i];
-    x.n_ent = a.topk ? a.k : max(0, L + d + 1 - W) >> p.ratio_log;
-    x.n_all = x.n_ent;
-    x.w0 = min(L, max(0, L + d + 1 - W));
-    x.n_win = L - x.w0;
-    x.n_tree = d + 1;
-  } else {
-    const int r0 = x.u * kR, rows = x.q.s.n * a.heads;
-    x.nrows = min(kR, rows - r0);
-    x.node0 = r0 / a.heads;
-    const int last = (r0 + x.nrows - 1) / a.heads;
-    x.row0 = (long long)x.q.s.first * a.heads + r0;
-    int lo = V4KV_MAX_TREE_NODES, hi = 0;
-    for (int i = x.node0; i <= last; ++i) {
-      const int d = p.w.depth[x.q.s.first + i];
-      lo = min(lo, d);
-      hi = max(hi, d);
-    }
-    x.n_ent = max(0, L + hi + 1 - W) >> p.ratio_log;
-    x.n_all = max(0, L + lo + 1 - W) >> p.ratio_log;
-    x.w0 = min(L, max(0, L + lo + 1 - W));
-    x.n_win = L - x.w0;
-    x.n_tree = last + 1;
-  }
+__device__ __forceinline__ void unit_load(const Params& p, Unit& x, int g) {
+  const int4* r = p.w.units + (size_t)g * 4;
+  const int4 a = r[0], b = r[1], c = r[2], d = r[3];
+  x.g = g;
+  x.tile = 0;
+  x.row0 = a.x; x.nrows = a.y; x.te = a.z; x.tr = a.w;
+  x.n_ent = b.x; x.n_all = b.y; x.w0 = b.z; x.n_win = b.w;
+  x.n_tree = c.x; x.node0 = c.y; x.first = c.z; x.L = c.w;
+  x.b = d.x; x.raw = d.y; x.raw_tree = d.z; x.next = d.w;
 }
 
-// next unit (after the last: b == batch)
-__device__ __noinline__ void unit_next(const Params& p, Unit& x) {
-  ++x.u;
-  x.tile = 0;
-  while (x.u >= x.q.units) {
-    x.u = 0;
-    if (++x.b >= p.a.batch) return;
-    x.q = plan_of(p, x.b, nullptr);
+// to the next tile, of the next unit after a unit's last
+__device__ __forceinline__ void tile_next(const Params& p, Unit& x) {
+  if (++x.tile == x.te + x.tr && x.next >= 0) unit_load(p, x, x.next);
+}
+
+// prep: unit u of sequence b, from the depths of the sequence's nodes
+__device__ __forceinline__ void unit_store(const Params& p, const SeqPlan& q, int b, int u, const int* depth, int next) {
+  const TreeArgs& a = p.a;
+  const int L = q.L, W = a.window_len;
+  int node0, nrows, row0, lo, hi, n_tree;
+  if (p.per_node) {
+    node0 = u / p.hc;
+    const int h0 = (u - node0 * p.hc) * kR;
+    nrows = min(kR, a.heads - h0);
+    row0 = (q.s.first + node0) * a.heads + h0;
+    lo = hi = depth[node0];
+    n_tree = lo + 1;
+  } else {
+    const int r0 = u * kR;
+    nrows = min(kR, q.s.n * a.heads - r0);
+    row0 = q.s.first * a.heads + r0;
+    node0 = r0 / a.heads;
+    const int last = (r0 + nrows - 1) / a.heads;
+    lo = V4KV_MAX_TREE_NODES;
+    hi = 0;
+    for (int i = node0; i <= last; ++i) {
+      lo = min(lo, depth[i]);
+      hi = max(hi, depth[i]);
+    }
+    n_tree = last + 1;
   }
-  unit_set(p, x);
+  const int w0 = min(L, max(0, L + lo + 1 - W)), base = (int)raw_row0(a, q, b) - raw_w0(a, q);
+  int4* r = p.w.units + (size_t)unit_index(p, q, b, u) * 4;
+  r[0] = make_int4(row0, nrows, q.te, q.tr);
+  r[1] = a.topk ? make_int4(a.k, a.k, w0, L - w0)
+                : make_int4(max(0, L + hi + 1 - W) >> p.ratio_log, max(0, L + lo + 1 - W) >> p.ratio_log, w0, L - w0);
+  r[2] = make_int4(n_tree, q.s.first + node0, q.s.first, L);
+  r[3] = make_int4(b, base + w0, base + L, next);
 }
 
 // A tile: whether its items are entries, the first one's index in its list,
@@ -244,8 +251,8 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_of(const Params& p, const Unit& x) {
   Tile t;
-  t.entries = x.tile < x.q.te;
-  t.first = (t.entries ? x.tile : x.tile - x.q.te) * kT;
+  t.entries = x.tile < x.te;
+  t.first = (t.entries ? x.tile : x.tile - x.te) * kT;
   t.count = min(kT, (t.entries ? x.n_ent : x.n_win + x.n_tree) - t.first);
   t.images = t.entries && p.a.main.dtype == V4KV_FP8_E4M3 ? 1 : 2;
   return t;
@@ -257,13 +264,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool named_or(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred a, b;\n\t"
       "setp.ne.u32 a, %1, 0;\n\t"
-      "bar.red.or.pred b, %2, 128, a;\n\t"
+      "bar.red.or.pred b, %2, 256, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)p), "r"(id)
@@ -339,6 +346,13 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
 }
 
+// 16 lanes x 16 columns: thread t gets, for k = 0, 1, r[4k + 0/1] = (lane t/4,
+// columns 8k + 2(t%4) + 0/1) and r[4k + 2/3] = (lane t/4 + 8, the same columns)
+__device__ __forceinline__ void tmem_ld16x256_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -349,6 +363,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
@@ -374,9 +392,7 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
                                              unsigned long long* rows, float4* meta) {
   const TreeArgs& a = p.a;
   if (!t.entries) {
-    const size_t base = raw_row0(a, x.q, x.b);
-    const int w0 = raw_w0(a, x.q);
-    const uint4 m4 = p.w.anc[x.q.s.first + x.node0];
+    const uint4 m4 = p.w.anc[x.node0];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int k = lane + 32 * r;
@@ -385,7 +401,7 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
       float2 mt = make_float2(0.f, -INFINITY);
       if (k < t.count) {
         if (n < x.n_win) {
-          n += x.w0 - w0;
+          n += x.raw;
         } else {
           n -= x.n_win;
           if (p.per_node) {  // the n-th of the node's ancestors
@@ -397,10 +413,10 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
             for (; n > 0; --n) m &= m - 1;
             n = up + __ffs(m) - 1;
           }
-          n += x.q.L - w0;
+          n += x.raw_tree;
         }
-        at = reinterpret_cast<unsigned long long>(p.w.raw) + (base + n) * (2 * kD);
-        mt = p.w.raw_meta[base + n];
+        at = reinterpret_cast<unsigned long long>(p.w.raw) + (size_t)n * (2 * kD);
+        mt = p.w.raw_meta[n];
       }
       rows[k] = at;
       meta[k] = item_meta(mt.x, mt.y == 0.f);
@@ -414,13 +430,13 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
   for (int r = 0; r < 4; ++r) {
     const int k = lane + 32 * r;
     j[r] = k < t.count ? t.first + k : -1;
-    if (a.topk && j[r] >= 0) j[r] = a.topk[(size_t)(x.q.s.first + x.node0) * a.k + j[r]];
+    if (a.topk && j[r] >= 0) j[r] = a.topk[(size_t)x.node0 * a.k + j[r]];
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     pg[r] = -1;
     if (j[r] < 0) continue;
-    if (a.topk && j[r] >= (x.q.L + a.ratio - 1) >> p.ratio_log) {
+    if (a.topk && j[r] >= (x.L + a.ratio - 1) >> p.ratio_log) {
       err |= V4KV_DEV_BAD_INDEX;
       j[r] = -1;
     } else if (j[r] >> p.spb_log >= pool.max_blocks) {
@@ -499,13 +515,13 @@ __device__ __noinline__ void load_bf16_rows(const unsigned long long* rows, int 
       raw[1] = p[2 * lane + 1];
     }
   };
-  uint4 raw[8][2];
+  uint4 raw[4][2];
 #pragma unroll
-  for (int k = 0; k < 6; ++k) get(k, raw[k]);
+  for (int k = 0; k < 2; ++k) get(k, raw[k]);
 #pragma unroll 1
   for (int r = 0; r < 32; r += 2) {
-    get(r + 6, raw[6]);
-    get(r + 7, raw[7]);
+    get(r + 2, raw[2]);
+    get(r + 3, raw[3]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r0 + r + k, lane & 7);
@@ -516,7 +532,7 @@ __device__ __noinline__ void load_bf16_rows(const unsigned long long* rows, int 
       *reinterpret_cast<uint4*>(lo_dst + off) = lo;
     }
 #pragma unroll
-    for (int k = 0; k < 6; ++k) {
+    for (int k = 0; k < 2; ++k) {
       raw[k][0] = raw[k + 2][0];
       raw[k][1] = raw[k + 2][1];
     }
@@ -550,18 +566,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       tc::mbar_init(&bars->addr_full[s], 32);
       tc::mbar_init(&bars->addr_free[s], 1);
     }
+    tc::mbar_init(&bars->ready, 4);
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 1);
     tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->s_free, 8);
-    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->s_free, 16);
+    tc::mbar_init(&bars->p_full, 16);
     tc::mbar_init(&bars->p_free, 1);
     tc::mbar_init(&bars->pv_done, 1);
     tc::mbar_init(&bars->drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 12) tc::tmem_alloc(tmem_slot, kCols);
+  if (warp == 20) tc::tmem_alloc(tmem_slot, kCols);
   tc::pdl_wait();
   tc::pdl_launch_dependents();
   tc::tc_fence_before();
@@ -571,17 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   const int4 rec = p.w.rec[blockIdx.x];
   const int n_tiles = p.w.rec[blockIdx.x + 1].x - rec.x;
   if (n_tiles <= 0) {
-    if (warp == 12) tc::tmem_free(tmem, kCols);
+    if (warp == 20) tc::tmem_free(tmem, kCols);
     return;
   }
   Unit x;
-  x.b = rec.y;
-  x.u = rec.z;
+  unit_load(p, x, rec.y);
   x.tile = rec.w;
-  x.q = plan_of(p, x.b, nullptr);
-  unit_set(p, x);
 
-  if (warp == 15) {
+  if (warp == 23) {
     // ======================= the units' Q, as their last one's products are done
     bool ok = true;
     uint32_t seg = 0;
@@ -593,12 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       }
       if (lane == 0) {
         tc::mbar_arrive_expect_tx(&bars->q_full, 65536);
-        const uint8_t* src = p.w.q + (size_t)q_image(p, x.q, x.b, x.u) * 65536;
+        const uint8_t* src = p.w.q + (size_t)x.g * 65536;
         for (int k = 0; k < 4; ++k)
           tc::bulk_load(sbase + kQOff + k * 16384, src + k * 16384, 16384, &bars->q_full);
       }
-      i += x.q.te + x.q.tr - x.tile;
-      if (i < n_tiles) unit_next(p, x);
+      i += x.te + x.tr - x.tile;
+      if (i < n_tiles) unit_load(p, x, x.next);
     }
     if (!ok) {
       *abort_flag = 1;
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     // the last copy has landed before the block's shared memory is released
     volatile int never = 0;
     if (seg > 0 && !tc::mbar_wait(&bars->q_full, (seg - 1) & 1, &never)) flag(a.dev_status, V4KV_DEV_TIMEOUT);
-  } else if (warp >= 13) {
+  } else if (warp >= 21) {
     // ======================= row addresses and scales, up to kRing tiles ahead.
     // Tile number `done` of the block (tiles without items do not count) is in
     // slot done % kRing.
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     for (int i = 0; i < n_tiles && ok; ++i) {
       const Tile t = tile_of(p, x);
       if (t.count > 0) {
-        if ((done & 1) == (uint32_t)(warp - 13)) {
+        if ((done & 1) == (uint32_t)(warp - 21)) {
           const uint32_t s = done % kRing;
           if (done >= kRing) ok = tc::mbar_wait(&bars->addr_free[s], ((done - kRing) / kRing) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) break;
@@ -625,16 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         }
         ++done;
       }
-      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      tile_next(p, x);
     }
     if (!ok) {
       *abort_flag = 1;
       flag(a.dev_status, V4KV_DEV_TIMEOUT);
     }
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= 16 && warp < 20) {
     // ======================= tiles into the stages. `im` counts images: image
     // im lives in stage im % 2.
-    const int w = warp - 8;
+    const int w = warp - 16;
     bool ok = true;
     uint32_t im = 0, done = 0;
     auto wait_empty = [&](uint32_t m, int c) {
@@ -648,25 +662,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         ok = tc::mbar_wait(&bars->addr_full[slot], (done / kRing) & 1, abort_flag);
         if (t.images == 1 && p.pages && t.first + kT <= x.n_all) {
           // two whole pages, every row of them visible: two boxes per 128 dims,
-          // as the last tile's product leaves them
-          int y = 0;
-          if (lane < 2) {
-            // a page that is missing is read behind the pool's end: zeros
-            const unsigned long long row = rows[64 * lane];
-            y = row ? (int)((row - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
-                    : a.main.num_pages * a.main.spb;
-          }
-          for (int c = 0; c < 4 && ok; ++c) {
-            ok = __all_sync(0xffffffffu, ok && wait_empty(im, c));
+          // as the last tile's product leaves them. The other warps only keep step.
+          if (w > 0) {
+            ok = __all_sync(0xffffffffu, ok && wait_empty(im, 3));
             if (!ok) break;
-            if (lane == 0) {
-              if (w == 0) tc::mbar_arrive_expect_tx(&bars->kv_full[s][c], kChunk);
-              else tc::mbar_arrive(&bars->kv_full[s][c]);
+          } else {
+            int y = 0;
+            if (lane < 2) {
+              // a page that is missing is read behind the pool's end: zeros
+              const unsigned long long row = rows[64 * lane];
+              y = row ? (int)((row - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
+                      : a.main.num_pages * a.main.spb;
             }
-            __syncwarp();
-            if (w == 0 && lane < 2)
-              tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + lane * (kChunk / 2), &p.map, 128 * c, y,
-                              &bars->kv_full[s][c]);
+            for (int c = 0; c < 4 && ok; ++c) {
+              ok = __all_sync(0xffffffffu, ok && wait_empty(im, c));
+              if (!ok) break;
+              if (lane == 0) {
+                mbar_arrive_n(&bars->kv_full[s][c], 3);
+                tc::mbar_arrive_expect_tx(&bars->kv_full[s][c], kChunk);
+              }
+              __syncwarp();
+              if (lane < 2)
+                tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + lane * (kChunk / 2), &p.map, 128 * c, y,
+                                &bars->kv_full[s][c]);
+            }
           }
         } else {
           for (int k = 0; k < t.images; ++k)
@@ -716,13 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         im += t.images;
         ++done;
       }
-      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      tile_next(p, x);
     }
     if (!ok) {
       *abort_flag = 1;
       flag(a.dev_status, V4KV_DEV_TIMEOUT);
     }
-  } else if (warp == 12) {
+  } else if (warp == 20) {
     // ======================= MMA issue: the whole warp runs the loop, one lane
     // elected once issues
     const bool leader = tc::elect_one();
@@ -766,8 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     bool s_issued = false;    // the current tile's S has been issued
     uint32_t filled = 0;      // O^T holds something of this segment
     Tile t = tile_of(p, x);
+    wait_all(&bars->ready, 0);  // the constant block scales are in tensor memory
+    tc::tc_fence_after();
     while (i < n_tiles && ok) {
-      const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
+      const bool seg_last = x.tile + 1 == x.te + x.tr || i + 1 == n_tiles;
       if (!opened) {
         wait_all(&bars->q_full, seg & 1);
         if (!ok) break;
@@ -778,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       if (seg_last && leader) tc::mma_commit(&bars->q_empty);
       __syncwarp();
       // the next tile, while the softmax works on this one
-      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      tile_next(p, x);
       const Tile nt = i + 1 < n_tiles ? tile_of(p, x) : Tile{false, 0, 0, 0};
       s_issued = false;
       if (t.count > 0 && ok) {
@@ -842,24 +863,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     if (!tc::mbar_wait(&bars->drain, 0, &never) && leader) flag(a.dev_status, V4KV_DEV_TIMEOUT);
     __syncwarp();
   } else {
-    // ======================= softmax: warp w of half hh has items 32 w .. 32 w +
-    // 31 and rows 32 hh .. 32 hh + 31; a thread items 32 w + lane / 4 + 8 j
-    // (j < 4) and rows 32 hh + 8 c + m (c = lane % 4, m < 8). That is how the
-    // 16x256b tensor-memory load deals out S when row 8 c + 2 k + e of a half
-    // sits in Q's row 8 k + 2 c + e. The eight rows' factors, references and
-    // sums fit in registers, and a row's maximum over the items takes three
-    // shuffles. The two halves meet only between units,
-    // at a barrier with a limit.
-    const int hh = warp >> 2, w = warp & 3, c4 = lane & 3;
+    // ======================= softmax: warp w of quarter qd has items 32 w .. 32 w
+    // + 31 and rows 16 qd .. 16 qd + 15; a thread items 32 w + lane / 4 + 8 j
+    // (j < 4) and rows 16 qd + 4 c + m (c = lane % 4, m < 4). That is how the
+    // 16x256b tensor-memory load deals out S when row 4 c + 2 k + e of a quarter
+    // sits in Q's row 8 k + 2 c + e: a row's maximum over the items takes three
+    // shuffles and the thread's part of P is four consecutive bytes of a row.
+    // The two quarters of a half meet at a barrier per tile.
+    const int qd = warp >> 2, w = warp & 3, c4 = lane & 3, hh = qd >> 1;
     const int bar = 1 + hh;
+    const int row_t = 16 * qd + 4 * c4;        // the thread's first row
+    const int row_h = row_t & 31;              // in its half
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     float* red = reinterpret_cast<float*>(sm + kRedOff) + 128 * hh;       // [4][32]
-    float* fac = reinterpret_cast<float*>(sm + kFacOff) + 32 * hh;        // [32]
+    float* fac = reinterpret_cast<float*>(sm + kFacOff);                  // [64]
     uint8_t* sf = sm + kSfOff + 128 * hh;                                  // [32][4]
     volatile int* raise = reinterpret_cast<volatile int*>(sm + kMiscOff + 16) + 2 * hh;
-    const uint4* anc = reinterpret_cast<const uint4*>(sm + kAncOff) + 32 * hh + 8 * c4;
-    const int4* vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh + 8 * c4;
-    if (hh == 0) {
+    const uint4* anc = reinterpret_cast<const uint4*>(sm + kAncOff) + row_t;
+    const int4* vis = reinterpret_cast<const int4*>(sm + kVisOff);
+    if (qd == 0) {
       const uint32_t one = 0x7f7f7f7fu, low = 0x7b7b7b7bu;
       tmem_st4(lanes + kOne, one, one, one, one);
       tmem_st4(lanes + kLow, low, low, low, low);
@@ -867,31 +889,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       tmem_st4(lanes + kSfHi, one, one, one, one);
       tmem_st4(lanes + kSfLo, one, one, one, one);
       tc::tmem_wait_st();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->ready);
     }
+    if (w == 0 && lane < 2 && !(qd & 1)) raise[lane] = 0;
     bool ok = true, seg_open = true, any = false;
     int seg_tile0 = 0;
     uint32_t done = 0, seg = 0;
-    float l[8], fa[8], ref[8];
-    if (w == 0 && lane < 2) raise[lane] = 0;
+    float l[4], fa[4], ref[4];
     for (int i = 0; i < n_tiles; ++i) {
       if (seg_open) {
         // the rows' factors, references and masks
         seg_open = false;
         any = false;
         seg_tile0 = x.tile;
-        const float* qf = p.w.q_factor + (size_t)q_image(p, x.q, x.b, x.u) * kR + 32 * hh + 8 * c4;
+        const float4 f = *reinterpret_cast<const float4*>(p.w.q_factor + (size_t)x.g * kR + row_t);
+        fa[0] = f.x; fa[1] = f.y; fa[2] = f.z; fa[3] = f.w;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < 4; ++m) {
           l[m] = 0.f;
-          fa[m] = qf[m];
           ref[m] = kNone;
         }
-        if (w == 0) {
-          const int n = 32 * hh + lane;
+        if (w == 0 && lane < 16) {
+          const int n = 16 * qd + lane;
           int node = x.node0;  // per_node: the only one
-          if (!p.per_node && n < x.nrows) node = (x.u * kR + n) / a.heads;
-          node += x.q.s.first;
-          const int w0 = max(0, x.q.L + p.w.depth[node] + 1 - a.window_len);
+          if (!p.per_node && n < x.nrows) node = (x.row0 + n) / a.heads;
+          const int w0 = max(0, x.L + p.w.depth[node] + 1 - a.window_len);
           reinterpret_cast<uint4*>(sm + kAncOff)[n] = p.w.anc[node];
           reinterpret_cast<int4*>(sm + kVisOff)[n] = make_int4(w0 >> p.ratio_log, w0, node, 0);
           row_ref[n] = kNone;
@@ -899,83 +923,86 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         named_sync(bar);
       }
       const Tile t = tile_of(p, x);
-      const bool seg_last = x.tile + 1 == x.q.te + x.q.tr || i + 1 == n_tiles;
+      const bool seg_last = x.tile + 1 == x.te + x.tr || i + 1 == n_tiles;
       if (t.count > 0) {
         ok = tc::mbar_wait_spin(&bars->s_full, done & 1, abort_flag, 32);
         tc::tc_fence_after();
         // the items' {scale, log2 |scale|, 1 / |scale|} and the scores u[j][m],
         // log2 of a weight of the item's codes
-        float u[4][8], inv[4];
-        uint32_t seen = 0;  // bit 8 j + m: row m sees item j
+        float u[4][4], inv[4];
+        uint32_t seen = 0;  // bit 4 j + m: row m sees item j
         bool plain = true;  // all scales positive
+        const float4* mts = meta + (done % kRing) * kT + 32 * w + (lane >> 2);
         {
+          uint32_t h[2][8], q[2][8];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            tmem_ld16x256_x2(lanes + ((uint32_t)(16 * k) << 16) + kSCol + 16 * qd, h[k]);
+            tmem_ld16x256_x2(lanes + ((uint32_t)(16 * k) << 16) + kSCol + kR + 16 * qd, q[k]);
+          }
           float ks[4], lg[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float4 mt = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j];
+            const float4 mt = mts[8 * j];
             ks[j] = mt.x;
             lg[j] = mt.y;
             inv[j] = mt.z;
-            seen |= (mt.w == 0.f ? 0xffu : 0u) << (8 * j);
+            seen |= (mt.w == 0.f ? 0xfu : 0u) << (4 * j);
             plain &= mt.x > 0.f;
           }
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t h[16], q[16];
-            tc::tmem_ld16x256_x4(lanes + ((uint32_t)(16 * k) << 16) + kSCol + 32 * hh, h);
-            tc::tmem_ld16x256_x4(lanes + ((uint32_t)(16 * k) << 16) + kSCol + kR + 32 * hh, q);
-            tc::tmem_wait_ld();
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int m = 0; m < 8; ++m) {
-                const int r = 4 * (m >> 1) + 2 * j + (m & 1);
-                u[2 * k + j][m] =
-                    fmaf((__uint_as_float(h[r]) + __uint_as_float(q[r])) * ks[2 * k + j], fa[m], lg[2 * k + j]);
-              }
-          }
+            for (int m = 0; m < 4; ++m) {
+              const int r = 4 * (m >> 1) + 2 * (j & 1) + (m & 1);
+              u[j][m] = fmaf((__uint_as_float(h[j >> 1][r]) + __uint_as_float(q[j >> 1][r])) * ks[j], fa[m], lg[j]);
+            }
         }
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->s_free);
         if (!p.per_node && (!t.entries || t.first + kT > x.n_all)) {
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 4; ++j) {
             const int r = t.first + 32 * w + (lane >> 2) + 8 * j;
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
+            for (int m = 0; m < 4; ++m) {
               bool v;
               if (t.entries) {
-                v = r < vis[m].x;
+                v = r < vis[row_t + m].x;
               } else if (r < x.n_win) {
-                v = x.w0 + r >= vis[m].y;
+                v = x.w0 + r >= vis[row_t + m].y;
               } else {
                 const int k = min(r - x.n_win, V4KV_MAX_TREE_NODES - 1);
                 v = (reinterpret_cast<const uint32_t*>(anc + m)[k >> 5] >> (k & 31)) & 1;
               }
-              if (!v) seen &= ~(1u << (8 * j + m));
+              if (!v) seen &= ~(1u << (4 * j + m));
             }
           }
         }
-        if (seen != 0xffffffffu) {
+        if (seen != 0xffffu) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-              if (!(seen >> (8 * j + m) & 1)) u[j][m] = -INFINITY;
+            for (int m = 0; m < 4; ++m)
+              if (!(seen >> (4 * j + m) & 1)) u[j][m] = -INFINITY;
         }
         // Per row, the exponent ex that puts the warp's 32 weights below 2^8,
-        // the largest in [2^7, 2^8): a weight is u = 2^ex times what is stored.
-        float ex[8], lt[8];
+        // the largest in [2^7, 2^8): a weight is 2^ex times what is stored.
+        float ex[4], lt[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) ex[m] = fmaxf(fmaxf(u[0][m], u[1][m]), fmaxf(u[2][m], u[3][m]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) ex[m] = fmaxf(ex[m], __shfl_xor_sync(0xffffffffu, ex[m], o));
         bool high = false;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          float mx = fmaxf(fmaxf(u[0][m], u[1][m]), fmaxf(u[2][m], u[3][m]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          ex[m] = mx == -INFINITY ? -INFINITY : floorf(mx) - 7.f;
+        for (int m = 0; m < 4; ++m) {
+          ex[m] = floorf(ex[m]) - 7.f;
           high |= ex[m] > ref[m] + kRaise;
-          const float c = mx == -INFINITY ? 0.f : ex[m];
+          const float c = ex[m] == -INFINITY ? 0.f : ex[m];
           lt[m] = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -987,11 +1014,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           // signs, and items of no value
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float ks = meta[(done % kRing) * kT + 32 * w + (lane >> 2) + 8 * j].x;
+            const float ks = mts[8 * j].x;
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-              u[j][m] = ks == 0.f ? 0.f : ks < 0.f ? -u[j][m] : u[j][m];
+            for (int m = 0; m < 4; ++m) u[j][m] = ks == 0.f ? 0.f : ks < 0.f ? -u[j][m] : u[j][m];
           }
+        }
+        uint32_t hw[4], lw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h0, h1, l0, l1;
+          split2(u[j][0], u[j][1], h0, l0);
+          split2(u[j][2], u[j][3], h1, l1);
+          hw[j] = h0 | (h1 << 16);
+          lw[j] = l0 | (l1 << 16);
         }
         if (__any_sync(0xffffffffu, high) && lane == 0) raise[done & 1] = 1;
         // the last tile's product has read P and its scales
@@ -1000,93 +1035,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           *abort_flag = 1;
           raise[done & 1] = 2;
         }
-        const uint32_t pcol = 2 * hh + (c4 >> 1), pbyte = 8 * (c4 & 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t hw[2], lw[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t h0, h1, l0, l1;
-            split2(u[j][4 * q], u[j][4 * q + 1], h0, l0);
-            split2(u[j][4 * q + 2], u[j][4 * q + 3], h1, l1);
-            hw[q] = h0 | (h1 << 16);
-            lw[q] = l0 | (l1 << 16);
-          }
           const int item = 32 * w + (lane >> 2) + 8 * j;
-          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, pcol) + pbyte) = make_uint2(hw[0], hw[1]);
-          *reinterpret_cast<uint2*>(sm + kPOff + tc::sw128_off(item, 4 + pcol) + pbyte) = make_uint2(lw[0], lw[1]);
+          *reinterpret_cast<uint32_t*>(sm + kPOff + tc::sw128_off(item, qd) + 4 * c4) = hw[j];
+          *reinterpret_cast<uint32_t*>(sm + kPOff + tc::sw128_off(item, 4 + qd) + 4 * c4) = lw[j];
         }
         // The block scales 2^(ex - ref), a byte per row and warp: lane
-        // (lane / 4, c) writes row 8 c + lane / 4.
+        // 4 m + c writes row 4 c + m of the quarter.
         auto put_scales = [&]() {
           float e = ex[0], r = ref[0];
 #pragma unroll
-          for (int m = 1; m < 8; ++m)
+          for (int m = 1; m < 4; ++m)
             if (lane >> 2 == m) {
               e = ex[m];
               r = ref[m];
             }
           const float d = e == -INFINITY ? -122.f : fminf(fmaxf(e - r, -122.f), 120.f);
-          sf[4 * (8 * c4 + (lane >> 2)) + w] = (uint8_t)((int)d + 127);
+          if (lane < 16) sf[4 * (row_h + (lane >> 2)) + w] = (uint8_t)((int)d + 127);
         };
         put_scales();
+        tc::fence_proxy_async_smem();
         named_sync(bar);
         const int up = raise[done & 1];
         if (up) {
-          if (up == 2) {  // a wait gave up: the four warps leave together
+          if (up == 2) {  // a wait gave up: the half's warps leave together
             ok = false;
             break;
           }
           // a row's weights passed its reference by 2^kRaise: raise it, and
           // O^T (the product before this tile is done), sums and scales with it
 #pragma unroll
-          for (int m = 0; m < 8; ++m)
-            if (lane < 4) red[32 * w + 8 * c4 + m] = ex[m];
+          for (int m = 0; m < 4; ++m)
+            if (lane < 4) red[32 * w + row_h + m] = ex[m];
           named_sync(bar);
-          if (w == 0 && lane == 0) raise[done & 1] = 0;
+          if (w == 0 && lane == 0 && !(qd & 1)) raise[done & 1] = 0;
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const int n = 8 * c4 + m;
+          for (int m = 0; m < 4; ++m) {
+            const int n = row_h + m;
             const float nm = fmaxf(fmaxf(fmaxf(red[n], red[32 + n]), fmaxf(red[64 + n], red[96 + n])), ref[m]);
             const float f = exp2f(ref[m] - nm);
             ref[m] = nm;
             l[m] *= f;
             if (w == 0 && lane < 4) {
-              fac[n] = f;
-              row_ref[32 * hh + n] = nm;
+              fac[row_t + m] = f;
+              row_ref[row_t + m] = nm;
             }
           }
           put_scales();
           named_sync(bar);
           if (any) {
 #pragma unroll 1
-            for (int g = 0; g < 16; ++g) {
-              const uint32_t at = lanes + kOCol + kR * (g >> 2) + 32 * hh + 8 * (g & 3);
+            for (int g = 0; g < 8; ++g) {
+              const int r0 = 16 * qd + 8 * (g & 1);
+              const uint32_t at = lanes + kOCol + kR * (g >> 1) + r0;
               uint32_t r8[8];
               tmem_ld8(at, r8);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int n = 0; n < 8; ++n) r8[n] = __float_as_uint(__uint_as_float(r8[n]) * fac[8 * (g & 3) + n]);
+              for (int n = 0; n < 8; ++n) r8[n] = __float_as_uint(__uint_as_float(r8[n]) * fac[r0 + n]);
               tmem_st8(at, r8);
             }
-            tc::tmem_wait_st();
           }
         }
         any = true;
+        // the two quarters write the hi and the lo terms' scales of the half
+        const uint32_t word = reinterpret_cast<const uint32_t*>(sf)[lane];
+        tmem_st1(lanes + (qd & 1 ? kSfLo : kSfHi) + hh, qd & 1 ? word - 0x04040404u : word);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < 4; ++m) {
           // 2^(ex - ref), an integer power below 2^41
           const float d = fmaxf(ex[m] - ref[m], -127.f);
           l[m] = fmaf(lt[m], __int_as_float(((int)d + 127) << 23), l[m]);
         }
-        const uint32_t word = reinterpret_cast<const uint32_t*>(sf)[lane];
-        tmem_st1(lanes + kSfHi + hh, word);
-        tmem_st1(lanes + kSfLo + hh, word - 0x04040404u);
-        tc::tmem_wait_st();
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->p_full);
         ++done;
       }
       if (seg_last) {
@@ -1099,74 +1124,68 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         ++seg;
         // the rows' sums over all items
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < 4; ++m) {
           float sum = l[m];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane < 4) red[32 * w + 8 * c4 + m] = sum;
+          if (lane < 4) red[32 * w + row_h + m] = sum;
         }
         named_sync(bar);
-        const bool whole = seg_tile0 == 0 && x.tile + 1 == x.q.te + x.q.tr;
+        const bool whole = seg_tile0 == 0 && x.tile + 1 == x.te + x.tr;
         // a block's first segment's partial result is its slot 0, its last one's slot 1
         const size_t slot = 2 * (size_t)blockIdx.x + (i + 1 - (x.tile + 1 - seg_tile0) > 0 ? 1 : 0);
-        if (w == 0) {
-          const float sum = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
-          fac[lane] = whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;  // a NaN stays one
-          if (!whole) p.w.part_ml[slot * kR + 32 * hh + lane] = make_float2(row_ref[32 * hh + lane], sum);
+        if (w == 0 && lane < 16) {
+          const int n = (16 * qd & 31) + lane;
+          const float sum = (red[n] + red[32 + n]) + (red[64 + n] + red[96 + n]);
+          fac[16 * qd + lane] = whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;  // a NaN stays one
+          if (!whole) p.w.part_ml[slot * kR + 16 * qd + lane] = make_float2(row_ref[16 * qd + lane], sum);
         }
         named_sync(bar);
-        // O^T: lane = dim 128 c + 32 w + lane, column = row
-        if (!whole) {
+        // O^T: lane = dim, column = row
+        const int pairs = a.rope.rope_dim >> 1;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r32[32];
-            tc::tmem_ld32(lanes + kOCol + kR * c + 32 * hh, r32);
-            tc::tmem_wait_ld();
-            float* o = p.w.part_o + (slot * kR + 32 * hh) * kD + 128 * c + 32 * w + lane;
+        for (int g = 0; g < 8; ++g) {
+          const int d = 128 * (g >> 1) + 32 * w + lane, r0 = 16 * qd + 8 * (g & 1);
+          const int pair = (d - a.rope.rope_offset) >> 1;
+          const bool rot = whole && d >= a.rope.rope_offset && pair < pairs;
+          uint32_t r8[8];
+          float v[8];
+          tmem_ld8(lanes + kOCol + kR * (g >> 1) + r0, r8);
+          tc::tmem_wait_ld();
 #pragma unroll
-            for (int n = 0; n < 32; ++n)
-              if (32 * hh + n < x.nrows) o[n * kD] = any ? __uint_as_float(r32[n]) : 0.f;
-          }
-        } else {
-          const int4* row_vis = reinterpret_cast<const int4*>(sm + kVisOff) + 32 * hh;
-          const int pairs = a.rope.rope_dim >> 1;
-#pragma unroll 1
-          for (int g = 0; g < 16; ++g) {
-            const int d = 128 * (g >> 2) + 32 * w + lane, pair = (d - a.rope.rope_offset) >> 1;
-            const bool rot = d >= a.rope.rope_offset && pair < pairs;
-            const int r0 = 8 * (g & 3);
-            uint32_t r8[8];
-            float v[8];
-            tmem_ld8(lanes + kOCol + kR * (g >> 2) + 32 * hh + r0, r8);
-            tc::tmem_wait_ld();
+          for (int n = 0; n < 8; ++n) v[n] = any ? __uint_as_float(r8[n]) * fac[r0 + n] : 0.f;
+          if (__any_sync(0xffffffffu, rot)) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) v[n] = any ? __uint_as_float(r8[n]) * fac[r0 + n] : 0.f;
-            if (__any_sync(0xffffffffu, rot)) {
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const float other = __shfl_xor_sync(0xffffffffu, v[n], 1);
-                if (rot) {
-                  const float2 f = p.w.rope[(size_t)row_vis[r0 + n].z * pairs + pair];
-                  v[n] = (d & 1) ? __fadd_rn(__fmul_rn(other, -f.y), __fmul_rn(v[n], f.x))
-                                 : __fsub_rn(__fmul_rn(v[n], f.x), __fmul_rn(other, -f.y));
-                }
+            for (int n = 0; n < 8; ++n) {
+              const float other = __shfl_xor_sync(0xffffffffu, v[n], 1);
+              if (rot) {
+                const float2 f = p.w.rope[(size_t)vis[r0 + n].z * pairs + pair];
+                v[n] = (d & 1) ? __fadd_rn(__fmul_rn(other, -f.y), __fmul_rn(v[n], f.x))
+                               : __fsub_rn(__fmul_rn(v[n], f.x), __fmul_rn(other, -f.y));
               }
             }
+          }
+          if (!whole) {
+            float* o = p.w.part_o + (slot * kR + r0) * kD + d;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              if (r0 + n < x.nrows) o[n * kD] = v[n];
+          } else {
             // even lanes store a pair of dims of rows r0 + 2 k, odd lanes of the row after
-            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (size_t)(x.row0 + 32 * hh + r0 + (lane & 1)) * kD + (d & ~1));
+            uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (size_t)(x.row0 + r0 + (lane & 1)) * kD + (d & ~1));
 #pragma unroll
             for (int n = 0; n < 8; n += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v[n] : v[n + 1], 1);
-              const float first = lane & 1 ? got : v[n], second = lane & 1 ? v[n + 1] : got;
-              if (32 * hh + r0 + n + (lane & 1) < x.nrows)
-                o[n * (kD / 2)] = float_to_bf16_bits(first) | ((uint32_t)float_to_bf16_bits(second) << 16);
+              const float lo = lane & 1 ? got : v[n], hi = lane & 1 ? v[n + 1] : got;
+              if (r0 + n + (lane & 1) < x.nrows)
+                o[n * (kD / 2)] = float_to_bf16_bits(lo) | ((uint32_t)float_to_bf16_bits(hi) << 16);
             }
           }
         }
         named_sync(bar);  // fac and the references are free
         seg_open = true;
       }
-      if (++x.tile == x.q.te + x.q.tr && i + 1 < n_tiles) unit_next(p, x);
+      tile_next(p, x);
     }
     if (!ok) {
       *abort_flag = 1;
@@ -1176,7 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
 
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     tc::tc_fence_after();
     tc::tmem_free(tmem, kCols);
   }
@@ -1191,15 +1210,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const int c = blockIdx.x;
   const int4 rec = p.w.rec[c];
   const int begin = rec.x - rec.w;  // the unit's first tile
-  if (c == 0 || rec.w == 0 || rec.y >= p.a.batch || p.w.rec[c - 1].x > begin) return;
+  if (c == 0 || rec.w == 0 || p.w.rec[c - 1].x > begin) return;
   const TreeArgs& a = p.a;
   Unit x;
-  x.b = rec.y;
-  x.u = rec.z;
-  x.tile = 0;
-  x.q = plan_of(p, x.b, nullptr);
-  unit_set(p, x);
-  const int end = begin + x.q.te + x.q.tr;
+  unit_load(p, x, rec.y);
+  const int end = begin + x.te + x.tr;
   const int row = 8 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= x.nrows) return;
   float acc[16], m = kNone, l = 0.f;
@@ -1272,6 +1287,19 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       depth[t] = d;
     }
     __syncthreads();
+    // the units, and behind the last one the next sequence's first
+    const SeqPlan plan = plan_of(p, b, nullptr);
+    for (int u = t; u < plan.units; u += 256) {
+      int next = unit_index(p, plan, b, u + 1);
+      if (u + 1 == plan.units) {
+        next = -1;
+        for (int bb = b + 1; bb < a.batch && next < 0; ++bb) {
+          const SeqPlan q = plan_of(p, bb, nullptr);
+          if (q.units > 0) next = unit_index(p, q, bb, 0);
+        }
+      }
+      unit_store(p, plan, b, u, depth, next);
+    }
     const int L = seq_len(a, b), pairs = a.rope.rope_dim >> 1;
     for (int k = t; k < s.n * pairs; k += 256) {
       const int i = k / pairs;
@@ -1283,8 +1311,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
   }
   const int raw_end = a.batch + 1 + a.batch * p.raw_blocks;
   if (b >= raw_end) {
-    // half a unit's Q: row 8 c + 2 k + e of a half at row 8 k + 2 c + e of the
-    // half (hi terms) and 64 rows on (lo terms)
+    // half a unit's Q: row 4 c + 2 k + e of a quarter at row 8 k + 2 c + e of it
+    // (hi terms) and 64 rows on (lo terms)
     const int g = (b - raw_end) >> 1, hh = (b - raw_end) & 1;
     const int bb = g / p.max_units, uu = g - bb * p.max_units;
     const SeqPlan q = plan_of(p, bb, nullptr);
@@ -1299,7 +1327,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       nrows = min(kR, q.s.n * a.heads - uu * kR);
       row0 = (size_t)q.s.first * a.heads + uu * kR;
     }
-    const int img = q_image(p, q, bb, uu);
+    const int img = unit_index(p, q, bb, uu);
     uint4 raw[kPrepRows][4];
 #pragma unroll
     for (int k = 0; k < kPrepRows; ++k) {
@@ -1333,8 +1361,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       m = __reduce_max_sync(0xffffffffu, m);
       uint4 hi, lo;
       split16(v, scale_up(m), hi, lo);
-      const int n = kPrepRows * warp + k;  // row of the half: 8 c + 2 k + e
-      const int at = 32 * hh + 8 * ((n >> 1) & 3) + 2 * (n >> 3) + (n & 1);
+      const int n = kPrepRows * warp + k;  // row of the half
+      const int at = 32 * hh + (n & 16) + 8 * ((n >> 1) & 1) + 2 * ((n >> 2) & 3) + (n & 1);
       uint8_t* dst = p.w.q + (size_t)img * 65536 + (lane >> 3) * kChunk;
       *reinterpret_cast<uint4*>(dst + tc::sw128_off(at, lane & 7)) = hi;
       *reinterpret_cast<uint4*>(dst + tc::sw128_off(kR + at, lane & 7)) = lo;
@@ -1443,7 +1471,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
   }
   const int blocks = min(p.grid, tcarry);
   for (int c = t; c <= p.grid; c += 256) {
-    int4 rec = make_int4(tcarry, a.batch, 0, 0);
+    int4 rec = make_int4(tcarry, 0, 0, 0);
     if (c < blocks) {
       const long long target = (long long)c * ccarry / blocks;
       int lo = 0, hi = a.batch - 1;  // the last sequence that begins at or before the target
@@ -1455,7 +1483,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       const int uc = unit_cost(p, q), n = q.te + q.tr;
       const long long off = target - p.w.cost[lo];
       const int u = (int)(off / uc), k = tile_at_cost(p, q, (int)(off % uc));
-      rec = make_int4(p.w.tiles[lo] + u * n + k, lo, u, k);
+      rec = make_int4(p.w.tiles[lo] + u * n + k, unit_index(p, q, lo, u), 0, k);
     }
     p.w.rec[c] = rec;
   }
@@ -1477,11 +1505,12 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
   x.anc = reinterpret_cast<uint4*>(take((size_t)total_nodes * sizeof(uint4)));
   x.depth = reinterpret_cast<int32_t*>(take((size_t)total_nodes * 4));
   x.rope = reinterpret_cast<float2*>(take((size_t)total_nodes * kPairs * sizeof(float2)));
-  // q_image() at most: whole units per node, or rows in units and one per sequence
+  // unit_index() at most: whole units per node, or rows in units and one per sequence
   const size_t images = heads % kR == 0 || k > 0 ? (size_t)total_nodes * ((heads + kR - 1) / kR)
                                                  : (size_t)total_nodes * heads / kR + batch + 1;
   x.q = take(images * 65536);
   x.q_factor = reinterpret_cast<float*>(take(images * kR * sizeof(float)));
+  x.units = reinterpret_cast<int4*>(take(images * 4 * sizeof(int4)));
   const size_t raws = (size_t)batch * (window_len - 1 < max_len ? window_len - 1 : max_len) + total_nodes;
   x.raw = take(raws * 2 * kD);
   x.raw_meta = reinterpret_cast<float2*>(take(raws * sizeof(float2)));
