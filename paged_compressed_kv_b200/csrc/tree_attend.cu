@@ -88,9 +88,10 @@ constexpr uint32_t kSfLo = 400;
 constexpr uint32_t kCols = 512;
 
 struct Bars {
-  uint64_t kv_full[2][4], kv_empty[2][4];  // per stage and 128 dims
+  uint64_t kv_full[2][4];   // per stage and 128 dims
+  uint64_t kv_empty[2][2];  // per stage and 256 dims
   uint64_t addr_full[kRing], addr_free[kRing];
-  uint64_t ready, q_full, q_empty, s_full, s_free, p_full, p_free, pv_done, drain;
+  uint64_t ready, q_full, q_empty, s_full, s_free, p_full, pv_done, drain;
 };
 static_assert(sizeof(Bars) <= 320, "barrier area");
 
@@ -365,10 +366,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
@@ -558,10 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < 8; ++s) {
-      tc::mbar_init(&bars->kv_full[s >> 2][s & 3], 4);
-      tc::mbar_init(&bars->kv_empty[s >> 2][s & 3], 1);
-    }
+    for (int s = 0; s < 8; ++s) tc::mbar_init(&bars->kv_full[s >> 2][s & 3], 4);
+    for (int s = 0; s < 4; ++s) tc::mbar_init(&bars->kv_empty[s >> 1][s & 1], 1);
     for (int s = 0; s < kRing; ++s) {
       tc::mbar_init(&bars->addr_full[s], 32);
       tc::mbar_init(&bars->addr_free[s], 1);
@@ -572,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->s_free, 16);
     tc::mbar_init(&bars->p_full, 16);
-    tc::mbar_init(&bars->p_free, 1);
     tc::mbar_init(&bars->pv_done, 1);
     tc::mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -633,7 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         if ((done & 1) == (uint32_t)(warp - 21)) {
           const uint32_t s = done % kRing;
           if (done >= kRing) ok = tc::mbar_wait(&bars->addr_free[s], ((done - kRing) / kRing) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
           resolve_tile(p, x, t, lane, reinterpret_cast<unsigned long long*>(sm + kPtrOff) + s * kT, meta + s * kT);
           tc::mbar_arrive(&bars->addr_full[s]);
         }
@@ -651,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     const int w = warp - 16;
     bool ok = true;
     uint32_t im = 0, done = 0;
+    // image m's place is free (the first 256 dims of it, then the others)
     auto wait_empty = [&](uint32_t m, int c) {
       return m < 2 || tc::mbar_wait(&bars->kv_empty[m & 1][c], ((m - 2) >> 1) & 1, abort_flag);
     };
@@ -662,34 +660,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         ok = tc::mbar_wait(&bars->addr_full[slot], (done / kRing) & 1, abort_flag);
         if (t.images == 1 && p.pages && t.first + kT <= x.n_all) {
           // two whole pages, every row of them visible: two boxes per 128 dims,
-          // as the last tile's product leaves them. The other warps only keep step.
-          if (w > 0) {
-            ok = __all_sync(0xffffffffu, ok && wait_empty(im, 3));
+          // as the last tile's product leaves them. All four warps wait and
+          // arrive, so that none falls a phase behind.
+          int y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            // a page that is missing is read behind the pool's end: zeros
+            y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
+                                : a.main.num_pages * a.main.spb;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if ((c & 1) == 0) ok = __all_sync(0xffffffffu, ok && wait_empty(im, c >> 1));
             if (!ok) break;
-          } else {
-            int y = 0;
-            if (lane < 2) {
-              // a page that is missing is read behind the pool's end: zeros
-              const unsigned long long row = rows[64 * lane];
-              y = row ? (int)((row - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
-                      : a.main.num_pages * a.main.spb;
-            }
-            for (int c = 0; c < 4 && ok; ++c) {
-              ok = __all_sync(0xffffffffu, ok && wait_empty(im, c));
-              if (!ok) break;
-              if (lane == 0) {
-                mbar_arrive_n(&bars->kv_full[s][c], 3);
+            if (lane == 0) {
+              if (w > 0) {
+                tc::mbar_arrive(&bars->kv_full[s][c]);
+              } else {
                 tc::mbar_arrive_expect_tx(&bars->kv_full[s][c], kChunk);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + k * (kChunk / 2), &p.map, 128 * c, y[k],
+                                  &bars->kv_full[s][c]);
               }
-              __syncwarp();
-              if (lane < 2)
-                tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + lane * (kChunk / 2), &p.map, 128 * c, y,
-                                &bars->kv_full[s][c]);
             }
           }
+          if (!ok) break;
         } else {
           for (int k = 0; k < t.images; ++k)
-            for (int c = 0; c < 4; ++c) ok = ok && wait_empty(im + k, c);
+            for (int c = 0; c < 2; ++c) ok = ok && wait_empty(im + k, c);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           float4* mt = meta + slot * kT;
@@ -751,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     bool ok = true;
     uint32_t im = 0;  // images before the current tile
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_spin(bar, parity, abort_flag));
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity, abort_flag));
     };
     // S^T of a tile whose images begin at `m`, 128 dims at a time as they land
     auto issue_s = [&](uint32_t m, int images) {
@@ -832,10 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
                   mma_mx(tmem + kOCol + kR * c, vm + (uint64_t)((c * kChunk + kk * 4096) >> 4),
                          p_l + (uint64_t)((kk * 4096) >> 4), idesc_mx(64, 1, kk), sfa, tmem + kSfLo, 1u);
                 }
-              tc::mma_commit(&bars->kv_empty[s][c]);
+              if (c & 1) tc::mma_commit(&bars->kv_empty[s][c >> 1]);
             }
           }
-          tc::mma_commit(&bars->p_free);
           tc::mma_commit(&bars->addr_free[done % kRing]);
         }
         __syncwarp();
@@ -896,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     if (w == 0 && lane < 2 && !(qd & 1)) raise[lane] = 0;
     bool ok = true, seg_open = true, any = false;
     int seg_tile0 = 0;
-    uint32_t done = 0, seg = 0;
+    uint32_t im = 0, done = 0, seg = 0;
     float l[4], fa[4], ref[4];
     for (int i = 0; i < n_tiles; ++i) {
       if (seg_open) {
@@ -925,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       const Tile t = tile_of(p, x);
       const bool seg_last = x.tile + 1 == x.te + x.tr || i + 1 == n_tiles;
       if (t.count > 0) {
-        ok = tc::mbar_wait_spin(&bars->s_full, done & 1, abort_flag, 32);
+        ok = tc::mbar_wait(&bars->s_full, done & 1, abort_flag);
         tc::tc_fence_after();
         // the items' {scale, log2 |scale|, 1 / |scale|} and the scores u[j][m],
         // log2 of a weight of the item's codes
@@ -1030,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         }
         if (__any_sync(0xffffffffu, high) && lane == 0) raise[done & 1] = 1;
         // the last tile's product has read P and its scales
-        if (done > 0) ok = ok && tc::mbar_wait(&bars->p_free, (done - 1) & 1, abort_flag);
+        if (im > 0) ok = ok && tc::mbar_wait(&bars->kv_empty[(im - 1) & 1][1], ((im - 1) >> 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok) && lane == 0) {
           *abort_flag = 1;
           raise[done & 1] = 2;
@@ -1112,6 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           const float d = fmaxf(ex[m] - ref[m], -127.f);
           l[m] = fmaf(lt[m], __int_as_float(((int)d + 127) << 23), l[m]);
         }
+        im += t.images;
         ++done;
       }
       if (seg_last) {
