@@ -449,8 +449,8 @@ v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total
  * fp64 (the order of a sum is fixed); a value that is not positive counts as 0.
  *   target      device [total_nodes, row_stride] of target_dtype (fp32 or
  *               bf16), row i the distribution after node i; vocab values used
- *   draft       the same of draft_dtype, row i the distribution node i's
- *               children were drawn from, or NULL
+ *   draft       the same (draft_dtype must be target_dtype), row i the
+ *               distribution node i's children were drawn from, or NULL
  *   row_stride  elements between rows, at least vocab
  *   tokens      device int32 [total_nodes]; a child whose token is outside
  *               [0, vocab) is flagged V4KV_DEV_BAD_INDEX and not accepted

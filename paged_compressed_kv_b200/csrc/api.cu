@@ -488,16 +488,16 @@ v4kv_status v4kv_tree_verify(const void* target, int32_t target_dtype, const voi
   if (!sample_u || !path_out || !n_path_out || !next_token) return V4KV_ERR_INVALID_ARG;
   if (total_nodes > 0 && (!target || !parents || !tokens || !accept_u)) return V4KV_ERR_INVALID_ARG;
   if (target_dtype != V4KV_FP32 && target_dtype != V4KV_BF16) return V4KV_ERR_INVALID_ARG;
-  if (draft && draft_dtype != V4KV_FP32 && draft_dtype != V4KV_BF16) return V4KV_ERR_INVALID_ARG;
+  if (draft && draft_dtype != target_dtype) return V4KV_ERR_INVALID_ARG;
   if (vocab < 1 || row_stride < vocab) return V4KV_ERR_INVALID_ARG;
   if ((target && !aligned16(target)) || (draft && !aligned16(draft))) return V4KV_ERR_INVALID_ARG;
-  v4kv_status st = check_device(nullptr);
+  int sms = 0;
+  v4kv_status st = check_device(&sms);
   if (st != V4KV_OK) return st;
   VerifyArgs a{};
   a.target = target;
   a.draft = draft;
   a.target_dtype = target_dtype;
-  a.draft_dtype = draft_dtype;
   a.vocab = vocab;
   a.row_stride = row_stride;
   a.batch = batch;
@@ -512,7 +512,7 @@ v4kv_status v4kv_tree_verify(const void* target, int32_t target_dtype, const voi
   a.n_path_out = n_path_out;
   a.next_token = next_token;
   a.dev_status = dev_status;
-  return to_status(launch_tree_verify(a, (cudaStream_t)stream));
+  return to_status(launch_tree_verify(a, sms, (cudaStream_t)stream));
 }
 
 v4kv_status v4kv_tree_gather(const void* x, const float* gate, int32_t dim, int32_t gate_dim,

@@ -167,8 +167,7 @@ struct TreeArgs {
 struct VerifyArgs {
   const void* target;
   const void* draft;  // or null: fixed guesses
-  int target_dtype;
-  int draft_dtype;
+  int target_dtype;  // of both
   int vocab;
   long long row_stride;
   int batch;
@@ -206,7 +205,7 @@ struct GatherArgs {
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
 size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int k, int window_len, int max_len,
                             int num_sms);
-cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_tree_gather(const GatherArgs& a, cudaStream_t stream);
 
 cudaError_t launch_slot_mapping(const int32_t* bt, int max_blocks, int batch,

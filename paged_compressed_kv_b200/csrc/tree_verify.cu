@@ -10,13 +10,14 @@
 // the node where the path ends (the next token's draw); every accept test
 // reads one value of p and q, all of them fetched up front.
 //
-// Bound: one row of p (and q) per sequence, 4 bytes a value, from HBM; for few
-// sequences the latency of the walk and of the exchange between blocks. A
-// cluster of 8 blocks takes each sequence, an eighth of the vocabulary each,
-// so that a single sequence's row is fetched by 8 SMs at once; the partial
-// sums cross through distributed shared memory. Sums are fp64: with 10^5
-// values whose prefix sum is compared with a given number, fp32 sums would
-// change the drawn token for about one draw in a hundred.
+// Bound: one row of p (and of q, where a draft was refused) per sequence, 4
+// bytes a value, from HBM; for few sequences the latency of the walk and of the
+// exchange between blocks. A cluster of 8 blocks takes each sequence, an eighth
+// of the vocabulary each, so that a single sequence's row is fetched by 8 SMs at
+// once, all of a warp's loads in flight together; the partial sums cross through
+// distributed shared memory. Sums are fp64: with 10^5 values whose prefix sum is
+// compared with a given number, fp32 sums would change the drawn token for about
+// one draw in a hundred.
 #include <cooperative_groups.h>
 
 #include "tc.cuh"
@@ -28,65 +29,69 @@ namespace v4kv {
 
 namespace {
 
-constexpr int kCluster = 8;          // blocks per sequence
+constexpr int kCluster = 8;          // blocks per sequence at most
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 
-__device__ __forceinline__ float value_at(const void* base, int dtype, size_t i) {
-  return dtype == V4KV_FP32 ? static_cast<const float*>(base)[i]
-                            : bf16_bits_to_float(static_cast<const uint16_t*>(base)[i]);
-}
+__device__ __forceinline__ float value_of(float x) { return x; }
+__device__ __forceinline__ float value_of(uint16_t x) { return bf16_bits_to_float(x); }
 
-// four consecutive values from a 16-byte (fp32) or 8-byte (bf16) aligned address
-__device__ __forceinline__ float4 value4_at(const void* base, int dtype, size_t i) {
-  if (dtype == V4KV_FP32) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+// four values from an address aligned to four of them
+__device__ __forceinline__ float4 four_at(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 four_at(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
 
-// One row as a sequence of groups of four values; the first group may begin
-// before the row (`lead` values of it belong to the row above), so that every
-// group is aligned whatever the row's offset.
+// What is left of a row: r = max(p - C q, 0), less the refused guesses. Values
+// that are not positive count as 0. `head` values come before the first group
+// of four that is aligned, `groups` such groups follow, then the row's last
+// values.
+template <typename T>
 struct Row {
-  const void *p, *q;      // bases of the arrays (q null: no draft)
-  int pt, qt;             // types
-  size_t at;              // element offset of the row
-  int lead, vocab, groups;
-  size_t limit;           // elements of the arrays (groups reaching past it load singly)
-  double C;               // r = max(p - C q, 0)
-  const int* gone;        // without a draft: refused tokens
+  const T *p, *q;  // q null: r = p
+  int vocab, head, groups;
+  double C;
+  const int* gone;
   int n_gone;
+
+  __device__ __forceinline__ double left(float pv, float qv, bool with_q) const {
+    double x = (double)fmaxf(pv, 0.f);
+    if (with_q) {
+      x = fma(-C, (double)fmaxf(qv, 0.f), x);
+      if (__double2hiint(x) < 0) x = 0.0;
+    }
+    return x;
+  }
+  __device__ __forceinline__ bool is_gone(int e) const {
+    bool hit = false;
+    for (int i = 0; i < n_gone; ++i) hit |= gone[i] == e;
+    return hit;
+  }
+  __device__ __forceinline__ double at(int e) const {
+    return is_gone(e) ? 0.0 : left(value_of(p[e]), q ? value_of(q[e]) : 0.f, q != nullptr);
+  }
+  __device__ __forceinline__ void group(int g, const float4& pv, const float4& qv, double* w, bool with_q) const {
+    w[0] = left(pv.x, qv.x, with_q);
+    w[1] = left(pv.y, qv.y, with_q);
+    w[2] = left(pv.z, qv.z, with_q);
+    w[3] = left(pv.w, qv.w, with_q);
+    for (int i = 0; i < n_gone; ++i) {
+      const int d = gone[i] - head - 4 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (d == k) w[k] = 0.0;
+    }
+  }
+  __device__ __forceinline__ double group_sum(int g, const float4& pv, const float4& qv, bool with_q) const {
+    double w[4];
+    group(g, pv, qv, w, with_q);
+    return (w[0] + w[1]) + (w[2] + w[3]);
+  }
 };
 
-__device__ __forceinline__ void group_weights(const Row& r, int g, double* w) {
-  const long long e0 = 4LL * g - r.lead;  // row index of the group's first value
-  float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-  if (e0 >= 0 && r.at + e0 + 4 <= r.limit) {
-    const float4 a = value4_at(r.p, r.pt, r.at + e0);
-    p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
-    if (r.q) {
-      const float4 b = value4_at(r.q, r.qt, r.at + e0);
-      q[0] = b.x; q[1] = b.y; q[2] = b.z; q[3] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = e0 + i >= 0 && e0 + i < r.vocab;
-      p[i] = in ? value_at(r.p, r.pt, r.at + e0 + i) : 0.f;
-      if (r.q && in) q[i] = value_at(r.q, r.qt, r.at + e0 + i);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const double x = r.q ? __dsub_rn((double)p[i], __dmul_rn(r.C, (double)q[i])) : (double)p[i];
-    w[i] = (e0 + i >= 0 && e0 + i < r.vocab && x > 0.0) ? x : 0.0;
-  }
-  for (int k = 0; k < r.n_gone; ++k) {
-    const long long d = r.gone[k] - e0;
-    if (d >= 0 && d < 4) w[d] = 0.0;
-  }
-}
+constexpr int kFlight = 4;  // groups a lane has in flight
 
 __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll
@@ -110,12 +115,15 @@ enum { kSumRow = 0, kDraw = 1 };
 
 }  // namespace
 
-// grid (kCluster * batch), clusters of kCluster blocks
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
+// A cluster of blocks per sequence, grid (blocks x batch). The code is kept short
+// (loops, one type per instance): a launch runs it once, and fetching it is a good
+// part of a small call.
+template <typename T>
+__global__ void __launch_bounds__(kVThreads, 2)
     tree_verify_kernel(VerifyArgs a) {
   __shared__ VerifyShared sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = blockIdx.x % kCluster, b = blockIdx.x / kCluster;
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / nc;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   tc::pdl_wait();
   tc::pdl_launch_dependents();
@@ -139,8 +147,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
     float p = 0.f, q = 1.f;
     if (parent >= 0 && ok) {
       const size_t at = (size_t)(s.first + parent) * a.row_stride + x;
-      p = value_at(a.target, a.target_dtype, at);
-      if (a.draft) q = value_at(a.draft, a.draft_dtype, at);
+      p = value_of(static_cast<const T*>(a.target)[at]);
+      if (a.draft) q = value_of(static_cast<const T*>(a.draft)[at]);
     }
     sh.parent[tid] = ok ? parent : -1;  // a child that cannot be accepted is never asked
     sh.token[tid] = x;
@@ -202,34 +210,56 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
       sh.task = task;
     }
     __syncthreads();
-    Row r;
-    r.p = a.target;
-    r.q = a.draft;
-    r.pt = a.target_dtype;
-    r.qt = a.draft_dtype;
-    r.at = (size_t)(s.first + sh.now) * a.row_stride;
-    r.lead = (int)(r.at & 3);
+    const size_t at = (size_t)(s.first + sh.now) * a.row_stride;
+    Row<T> r;
+    r.p = static_cast<const T*>(a.target) + at;
+    r.q = a.draft && sh.C != 0.0 ? static_cast<const T*>(a.draft) + at : nullptr;  // nothing was refused: r = p
     r.vocab = a.vocab;
-    r.groups = (a.vocab + r.lead + 3) / 4;
-    r.limit = (size_t)(a.total_nodes - 1) * a.row_stride + a.vocab;
+    r.head = min(a.vocab, (int)((4 - (at & 3)) & 3));
+    r.groups = (a.vocab - r.head) / 4;
     r.C = sh.C;
     r.gone = sh.gone;
     r.n_gone = sh.n_gone;
     const int task = sh.task;
-    // each warp of the cluster takes a run of consecutive groups
-    const int per = (r.groups + kCluster * kVWarps - 1) / (kCluster * kVWarps);
-    const int g0 = min(r.groups, (rank * kVWarps + warp) * per), g1 = min(r.groups, g0 + per);
+    // each warp of the cluster takes a run of consecutive groups, the first one
+    // the values before them too, the last one the values behind them
+    const int run_id = rank * kVWarps + warp;
+    const int per = (r.groups + nc * kVWarps - 1) / (nc * kVWarps);
+    const int g0 = min(r.groups, run_id * per), g1 = min(r.groups, g0 + per);
+    // the lane's odd value, if any: lanes 0 .. 2 of the first and last warps
+    int odd = -1;
+    if (run_id == 0 && lane < r.head) odd = lane;
+    const int back = r.head + 4 * r.groups;
+    if (run_id == nc * kVWarps - 1 && lane >= 4 && back + lane - 4 < r.vocab) odd = back + lane - 4;
     double total = 0.0, before = 0.0;
     int owner = 0;  // the block whose part the target falls in
     double target = 0.0;
     // the draw falls back to the whole row when nothing is left of it
     for (int attempt = 0; attempt < 2; ++attempt, ++exchange) {
-      double sum = 0.0;
-#pragma unroll 4
-      for (int g = g0 + lane; g < g1; g += 32) {
-        double w[4];
-        group_weights(r, g, w);
-        sum += (w[0] + w[1]) + (w[2] + w[3]);
+      double sum = odd >= 0 ? r.at(odd) : 0.0;
+      // 32 values of a lane in flight, of p alone or of p and q
+      if (!r.q) {
+#pragma unroll 1
+        for (int g = g0 + lane; g - lane < g1; g += 64 * kFlight) {
+          float4 pv[2 * kFlight];
+#pragma unroll
+          for (int k = 0; k < 2 * kFlight; ++k) pv[k] = four_at(r.p + r.head + 4 * (size_t)min(g + 32 * k, g1 - 1));
+#pragma unroll
+          for (int k = 0; k < 2 * kFlight; ++k)
+            if (g + 32 * k < g1) sum += r.group_sum(g + 32 * k, pv[k], pv[k], false);
+        }
+      } else {
+#pragma unroll 1
+        for (int g = g0 + lane; g - lane < g1; g += 32 * kFlight) {
+          float4 pv[kFlight], qv[kFlight];
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) pv[k] = four_at(r.p + r.head + 4 * (size_t)min(g + 32 * k, g1 - 1));
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) qv[k] = four_at(r.q + r.head + 4 * (size_t)min(g + 32 * k, g1 - 1));
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k)
+            if (g + 32 * k < g1) sum += r.group_sum(g + 32 * k, pv[k], qv[k], true);
+        }
       }
       sum = warp_sum_d(sum);
       if (lane == 0) sh.warp_part[warp] = sum;
@@ -237,18 +267,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
       // Two tables in turn: a block writes a table again two exchanges later,
       // behind a barrier that every block reached after reading it.
       double* part = sh.part[exchange & 1];
-      if (tid < kCluster) {
+      if (tid < nc) {
         double t = 0.0;
         for (int w = 0; w < kVWarps; ++w) t += sh.warp_part[w];
         *cluster.map_shared_rank(part + rank, tid) = t;
       }
       cluster.sync();
       total = 0.0;
-      for (int k = 0; k < kCluster; ++k) total += part[k];
+      for (int k = 0; k < nc; ++k) total += part[k];
       target = __dmul_rn((double)a.sample_u[b], total);
       double run = 0.0;
       owner = -1;
-      for (int k = 0; k < kCluster && (owner < 0 || run <= target); ++k) {
+      for (int k = 0; k < nc && (owner < 0 || run <= target); ++k) {
         // the first part that ends above the target; rounding may put the
         // target at the total, then the last part with a positive value
         if (part[k] > 0.0) {
@@ -259,6 +289,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
       }
       if (task == kSumRow || total > 0.0 || (r.C == 0.0 && r.n_gone == 0)) break;
       r.C = 0.0;
+      r.q = nullptr;
       r.n_gone = 0;
     }
     if (task == kSumRow) {
@@ -279,32 +310,58 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVThreads)
         run += sh.warp_part[w];
       }
       if (warp == w_own) {
+        // 32 groups at a time: their prefix sums over the lanes, then the group
+        // that ends above the target. The row's first values come before the
+        // first step, its last ones after the last.
         int found = -1, last = -1;
         run = start;
-        for (int g = g0; g < g1 && found < 0; g += 32) {
+        const int steps = (g1 - g0 + 31) / 32;
+        float4 pn = make_float4(0.f, 0.f, 0.f, 0.f), qn = pn;
+        auto fetch = [&](int i) {
+          if (i < 0 || i >= steps) return;
+          const size_t e = r.head + 4 * (size_t)min(g0 + 32 * i + lane, g1 - 1);
+          pn = four_at(r.p + e);
+          if (r.q) qn = four_at(r.q + e);
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int i = -1; i <= steps && found < 0; ++i) {
+          const int g = g0 + 32 * i + lane;
+          const bool inner = i >= 0 && i < steps;
+          const bool mine = inner ? g < g1 : odd >= 0 && (odd < r.head) == (i < 0);
+          const int first = inner ? r.head + 4 * g : odd;
           double w[4] = {0.0, 0.0, 0.0, 0.0};
-          if (g + lane < g1) group_weights(r, g + lane, w);
-          const double own = (w[0] + w[1]) + (w[2] + w[3]);
+          if (inner) {
+            r.group(g, pn, qn, w, r.q != nullptr);
+            fetch(i + 1);
+          } else if (mine) {
+            w[0] = r.at(odd);
+          }
+          const double own = mine ? (w[0] + w[1]) + (w[2] + w[3]) : 0.0;
           double incl = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
           }
-          double pre = run + (incl - own);
-          int pick = -1, pos = -1;
+          const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+          const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && run + incl > target);
+          if (any) {
+            // the first lane that ends above the target, else the last with a value
+            const int at_lane = over ? __ffs(over) - 1 : 31 - __clz(any);
+            double pre = run + (incl - own);
+            int pick = -1, pos = -1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            pre += w[i];
-            if (w[i] > 0.0) {
-              pos = 4 * (g + lane) - r.lead + i;
-              if (pick < 0 && pre > target) pick = pos;
+            for (int k = 0; k < 4; ++k) {
+              pre += w[k];
+              if (w[k] > 0.0) {
+                pos = first + k;
+                if (pick < 0 && pre > target) pick = pos;
+              }
             }
+            last = __shfl_sync(0xffffffffu, pos, at_lane);
+            if (over) found = __shfl_sync(0xffffffffu, pick >= 0 ? pick : pos, at_lane);
           }
-          const unsigned hit = __ballot_sync(0xffffffffu, pick >= 0);
-          if (hit) found = __shfl_sync(0xffffffffu, pick, __ffs(hit) - 1);
-          const unsigned any = __ballot_sync(0xffffffffu, pos >= 0);
-          if (any) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
           run += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) a.next_token[b] = found >= 0 ? found : last;
@@ -376,8 +433,28 @@ __global__ void __launch_bounds__(kGWarps * 32) tree_gather_kernel(GatherArgs a)
   }
 }
 
-cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
-  return launch_pdl(tree_verify_kernel, dim3((unsigned)a.batch * kCluster), dim3(kVThreads), 0, stream, a);
+// Blocks per sequence: 8 while the batch then fits the GPU at two blocks per SM
+// (one sequence's row is fetched by 8 SMs), 4 or 2 for larger ones, so that one
+// wave does. 64 sequences, 131072 values: 26.8 us at 8 blocks (two waves),
+// 24.0 us at 4.
+cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream) {
+  int nc = kCluster;
+  while (nc > 2 && (long long)a.batch * nc > 2LL * num_sms) nc /= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.batch * nc);
+  cfg.blockDim = dim3(kVThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = nc;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, a.target_dtype == V4KV_FP32 ? tree_verify_kernel<float> : tree_verify_kernel<uint16_t>,
+                            a);
 }
 
 cudaError_t launch_tree_gather(const GatherArgs& a, cudaStream_t stream) {

@@ -456,8 +456,9 @@ def v4kv_tree_verify(target, cu_nodes, parents, tokens, accept_u, sample_u, max_
     if sample_u.shape[0] != batch or n_path_out.shape[0] != batch or next_token.shape[0] != batch or \
             tuple(path_out.shape) != (batch, max_nodes):
         raise ValueError("sample_u, n_path_out, next_token and path_out must have one row per sequence")
-    if draft is not None and (_row_stride(draft, "draft") != stride or draft.shape != target.shape):
-        raise ValueError("draft must have target's shape and row stride")
+    if draft is not None and (_row_stride(draft, "draft") != stride or draft.shape != target.shape or
+                              draft.dtype != target.dtype):
+        raise ValueError("draft must have target's type, shape and row stride")
     code = {torch.float32: V4KV_FP32, torch.bfloat16: V4KV_BF16}
     st = _lib.v4kv_tree_verify(
         target.data_ptr(), code[target.dtype], _ptr(draft), code[draft.dtype] if draft is not None else 0,
