@@ -500,39 +500,20 @@ __device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& l
   return scale_down(m);
 }
 
-// 32 bf16 rows, the whole warp: lane takes dims 16 lane .. 16 lane + 15 of each;
-// the next rows' loads fly while two are split
-__device__ __noinline__ void load_bf16_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
-                                            uint8_t* lo_dst, float4* meta) {
-  auto get = [&](int r, uint4* raw) {
-    const uint4* p = reinterpret_cast<const uint4*>(r < 32 ? rows[r] : 0ull);
-    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-    if (p) {
-      raw[0] = p[2 * lane];
-      raw[1] = p[2 * lane + 1];
-    }
-  };
-  uint4 raw[4][2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) get(k, raw[k]);
-#pragma unroll 1
-  for (int r = 0; r < 32; r += 2) {
-    get(r + 2, raw[2]);
-    get(r + 3, raw[3]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r0 + r + k, lane & 7);
-      uint4 hi, lo;
-      const float scale = split_row(raw[k], hi, lo);
-      if (rows[r + k] && lane == 0) meta[r0 + r + k] = item_meta(scale, true);
-      *reinterpret_cast<uint4*>(hi_dst + off) = hi;
-      *reinterpret_cast<uint4*>(lo_dst + off) = lo;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      raw[k][0] = raw[k + 2][0];
-      raw[k][1] = raw[k + 2][1];
-    }
+// The rows' lanes' 32 bytes of bf16 that were copied to where the lane's two
+// terms go: split in place, `n` rows from r0 on.
+__device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, int n, int lane, uint8_t* hi_dst,
+                                        uint8_t* lo_dst, float4* meta) {
+#pragma unroll 2
+  for (int r = r0; r < r0 + n; ++r) {
+    const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r, lane & 7);
+    uint4 raw[2], hi, lo;
+    raw[0] = *reinterpret_cast<uint4*>(hi_dst + off);
+    raw[1] = *reinterpret_cast<uint4*>(lo_dst + off);
+    const float scale = split_row(raw, hi, lo);
+    if (rows[r] && lane == 0) meta[r] = item_meta(scale, true);
+    *reinterpret_cast<uint4*>(hi_dst + off) = hi;
+    *reinterpret_cast<uint4*>(lo_dst + off) = lo;
   }
 }
 
@@ -713,18 +694,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
               }
               *reinterpret_cast<uint4*>(dst + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7)) = v;
             }
-          } else if (!t.entries) {
+          } else {
+            // raw rows: their two terms. bf16 entries: the lane's 32 bytes.
+            const uint32_t step = t.entries ? 32 : 16, second = t.entries ? 16 : kD;
 #pragma unroll 8
             for (int r = 0; r < 32; ++r) {
               const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[32 * w + r]);
               const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7);
-              cp_async16(d0 + off, src ? src + 16 * lane : p.w.raw, src != nullptr);
-              cp_async16(d1 + off, src ? src + kD + 16 * lane : p.w.raw, src != nullptr);
+              const uint8_t* from = src ? src + step * lane : p.w.raw;
+              cp_async16(d0 + off, from, src != nullptr);
+              cp_async16(d1 + off, src ? from + second : from, src != nullptr);
             }
-          } else {
-            load_bf16_rows(rows + 32 * w, 32 * w, lane, dst, sm + kVOff + (s ^ 1) * kStage, mt);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
+          if (t.images == 2 && t.entries)
+            split_rows(rows, 32 * w, 32, lane, dst, sm + kVOff + (s ^ 1) * kStage, mt);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane < 4)
@@ -750,6 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     uint32_t im = 0;  // images before the current tile
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity, abort_flag));
+    };
+    auto poll = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_poll(bar, parity)); };
+    auto poll_kv = [&](uint32_t m) {
+      bool all = true;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) all = all && tc::mbar_poll(&bars->kv_full[m & 1][c], (m >> 1) & 1);
+      return __all_sync(0xffffffffu, all);
     };
     // S^T of a tile whose images begin at `m`, 128 dims at a time as they land
     auto issue_s = [&](uint32_t m, int images) {
@@ -801,16 +792,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       const Tile nt = i + 1 < n_tiles ? tile_of(p, x) : Tile{false, 0, 0, 0};
       s_issued = false;
       if (t.count > 0 && ok) {
-        if (!seg_last && nt.count > 0 && t.images == 1 && nt.images == 1) {
-          // its S too, once the softmax has taken this one's out of tensor memory
-          wait_all(&bars->s_free, done & 1);
-          if (ok) {
+        // Whichever is ready first: this tile's P, or the next tile with S free
+        // in tensor memory (the softmax has read this one's).
+        bool ahead = !seg_last && nt.count > 0 && t.images == 1 && nt.images == 1;
+        const long long t0 = clock64();
+        while (true) {
+          if (ahead && poll(&bars->s_free, done & 1) && poll_kv(im + 1)) {
             tc::tc_fence_after();
             issue_s(im + 1, 1);
             s_issued = true;
+            ahead = false;
+            if (!ok) break;
           }
+          if (ahead ? poll(&bars->p_full, done & 1)
+                    : __all_sync(0xffffffffu, tc::mbar_wait(&bars->p_full, done & 1, abort_flag)))
+            break;
+          if (!ahead || *abort_flag || clock64() - t0 > tc::kWaitCycles) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
-        wait_all(&bars->p_full, done & 1);
         if (!ok) break;
         tc::tc_fence_after();
         if (leader) {
