@@ -279,12 +279,38 @@ __device__ __forceinline__ bool named_or(int id, bool p) {
   return r != 0;
 }
 
+using f2 = unsigned long long;  // two fp32 values
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // two e4m3 terms of a pair: x = hi + lo / 16
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const uint16_t h = float2_to_e4m3x2(x, y);
-  const float2 f = __half22float2(e4m3x2_to_half2(h));
+  const __half2 r = __hmul2(__hsub2(__floats2half2_rn(x, y), e4m3x2_to_half2(h)), __float2half2_rn(16.f));
   hi = h;
-  lo = float2_to_e4m3x2((x - f.x) * 16.f, (y - f.y) * 16.f);
+  __half2_raw rr = *reinterpret_cast<const __half2_raw*>(&r);
+  lo = __nv_cvt_halfraw2_to_fp8x2(rr, __NV_SATFINITE, __NV_E4M3);
 }
 
 // the terms of 16 consecutive values times m
@@ -951,9 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int r = 4 * (m >> 1) + 2 * (j & 1) + (m & 1);
-              u[j][m] = fmaf((__uint_as_float(h[j >> 1][r]) + __uint_as_float(q[j >> 1][r])) * ks[j], fa[m], lg[j]);
+            for (int m = 0; m < 4; m += 2) {
+              const int r = 4 * (m >> 1) + 2 * (j & 1);
+              const f2 sum = add2(pack2(__uint_as_float(h[j >> 1][r]), __uint_as_float(h[j >> 1][r + 1])),
+                                  pack2(__uint_as_float(q[j >> 1][r]), __uint_as_float(q[j >> 1][r + 1])));
+              unpack2(fma2(mul2(sum, pack2(ks[j], ks[j])), pack2(fa[m], fa[m + 1]), pack2(lg[j], lg[j])), u[j][m],
+                      u[j][m + 1]);
             }
         }
         tc::tc_fence_before();
@@ -999,13 +1028,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         for (int m = 0; m < 4; ++m) {
           ex[m] = floorf(ex[m]) - 7.f;
           high |= ex[m] > ref[m] + kRaise;
-          const float c = ex[m] == -INFINITY ? 0.f : ex[m];
-          lt[m] = 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; m += 2) {
+          const f2 c = pack2(ex[m] == -INFINITY ? 0.f : -ex[m], ex[m + 1] == -INFINITY ? 0.f : -ex[m + 1]);
+          f2 sum = pack2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            u[j][m] = fast_exp2(u[j][m] - c);
-            lt[m] = fmaf(u[j][m], inv[j], lt[m]);
+            unpack2(add2(pack2(u[j][m], u[j][m + 1]), c), u[j][m], u[j][m + 1]);
+            u[j][m] = fast_exp2(u[j][m]);
+            u[j][m + 1] = fast_exp2(u[j][m + 1]);
+            sum = fma2(pack2(u[j][m], u[j][m + 1]), pack2(inv[j], inv[j]), sum);
           }
+          unpack2(sum, lt[m], lt[m + 1]);
         }
         if (__any_sync(0xffffffffu, !plain)) {
           // signs, and items of no value
@@ -1052,8 +1087,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           if (lane < 16) sf[4 * (row_h + (lane >> 2)) + w] = (uint8_t)((int)d + 127);
         };
         put_scales();
-        tc::fence_proxy_async_smem();
         named_sync(bar);
+        tc::fence_proxy_async_smem();
         const int up = raise[done & 1];
         if (up) {
           if (up == 2) {  // a wait gave up: the half's warps leave together

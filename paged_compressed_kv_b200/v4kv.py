@@ -390,51 +390,80 @@ def v4kv_tree_workspace_size(batch, heads, total_nodes, max_nodes, max_seq_len, 
     return out.value
 
 
+# These calls are short on the GPU, so their checks are kept short too: one pass
+# over a tensor's properties gives its pointer, and only a failed one is looked
+# into for its message.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t, what, stream):
+    """The first tensor's device, which has to be the current one, and the
+    stream's handle on it."""
+    if t is None or not t.is_cuda:
+        _need(t, (), what)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current device")
+    if stream is not None or _raw_stream is None:
+        return dev, _stream(stream)
+    return dev, _raw_stream(dev)
+
+
+def _at(t, dtype, ndim, dev, what):
+    """The pointer of a contiguous tensor of `dtype` on the current device."""
+    if t is not None and t.dtype is dtype and t.dim() == ndim and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, (dtype,), what, ndim)
+    raise ValueError(f"{what} must be on the current device")
+
+
 def v4kv_tree_attention(q, cu_nodes, parents, k_tree, main, window, seq_lens, max_nodes, max_seq_len, ratio,
                         window_len, out, workspace, topk=None, sm_scale=None, rope=None, dev_status=None,
                         stream=None):
     """Decode attention of every node of the sequences' drafted-token trees:
     q and out [total_nodes, heads, 512], k_tree [total_nodes, 512] the nodes'
     own rows, parents the index of each node's parent within its sequence."""
-    _need(q, (torch.float32, torch.bfloat16), "q", ndim=3)
-    _need(cu_nodes, (torch.int32,), "cu_nodes", ndim=1)
-    _need(parents, (torch.int32,), "parents", ndim=1)
-    _need(k_tree, (torch.bfloat16,), "k_tree", ndim=2)
-    _need(seq_lens, (torch.int32,), "seq_lens", ndim=1)
-    _need(out, (torch.bfloat16,), "out", ndim=3)
-    _need(workspace, (torch.uint8,), "workspace")
-    n = q.shape[0]
+    dev, stream = _here(q, "q", stream)
+    fp32 = q.dtype is torch.float32
+    qp = _at(q, torch.float32 if fp32 else torch.bfloat16, 3, dev, "q")
+    n, heads, dim = q.shape
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    if parents.shape[0] != n or tuple(k_tree.shape) != (n, q.shape[2]):
+    if parents.shape != (n,) or k_tree.shape != (n, dim):
         raise ValueError("parents and k_tree must have one row per node")
-    if cu_nodes.shape[0] != seq_lens.shape[0] + 1:
+    batch = seq_lens.shape[0]
+    if cu_nodes.shape[0] != batch + 1:
         raise ValueError("cu_nodes must have one value more than seq_lens")
-    if topk is not None:
-        _need(topk, (torch.int32,), "topk", ndim=2)
-        if topk.shape[0] != n:
-            raise ValueError("topk must have one row per node")
+    if topk is not None and topk.shape[0] != n:
+        raise ValueError("topk must have one row per node")
     rope = rope or Rope()
     mc, wc = main.c(), window.c()
     st = _lib.v4kv_tree_attention(
-        q.data_ptr(), V4KV_FP32 if q.dtype == torch.float32 else V4KV_BF16, seq_lens.shape[0], q.shape[1],
-        cu_nodes.data_ptr(), n, max_nodes, parents.data_ptr(), k_tree.data_ptr(), ctypes.byref(mc),
-        ctypes.byref(wc), seq_lens.data_ptr(), max_seq_len, ratio, window_len, _ptr(topk),
-        topk.shape[1] if topk is not None else 0, 0.0 if sm_scale is None else sm_scale, rope.c(),
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream))
-    _check("v4kv_tree_attention", st)
+        qp, V4KV_FP32 if fp32 else V4KV_BF16, batch, heads, _at(cu_nodes, torch.int32, 1, dev, "cu_nodes"), n,
+        max_nodes, _at(parents, torch.int32, 1, dev, "parents"), _at(k_tree, torch.bfloat16, 2, dev, "k_tree"),
+        ctypes.byref(mc), ctypes.byref(wc), _at(seq_lens, torch.int32, 1, dev, "seq_lens"), max_seq_len, ratio,
+        window_len, None if topk is None else _at(topk, torch.int32, 2, dev, "topk"),
+        0 if topk is None else topk.shape[1], 0.0 if sm_scale is None else sm_scale, rope.c(),
+        _at(out, torch.bfloat16, 3, dev, "out"), _at(workspace, torch.uint8, 1, dev, "workspace"),
+        workspace.shape[0], None if dev_status is None else _at(dev_status, torch.int32, 1, dev, "dev_status"),
+        stream)
+    if st != V4KV_OK:
+        raise V4KVError("v4kv_tree_attention", st)
 
 
-def _row_stride(t, what):
-    if t is None:
-        raise ValueError(f"{what} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype not in (torch.float32, torch.bfloat16):
+def _rows_at(t, dev, what):
+    """Pointer and row stride of [nodes, vocab] probabilities."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a CUDA tensor on the current device")
+    if t.dtype is not torch.float32 and t.dtype is not torch.bfloat16:
         raise ValueError(f"{what} has dtype {t.dtype}, expected float32 or bfloat16")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{what} must be [nodes, vocab] with consecutive values in a row")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dim() == 2:
+        n, vocab = t.shape
+        row, step = t.stride()
+        if (vocab <= 1 or step == 1) and (n <= 1 or row >= vocab):
+            return t.data_ptr(), row if n > 1 else vocab
+    raise ValueError(f"{what} must be [nodes, vocab] with consecutive values in a row")
 
 
 def v4kv_tree_verify(target, cu_nodes, parents, tokens, accept_u, sample_u, max_nodes, path_out, n_path_out,
@@ -442,56 +471,55 @@ def v4kv_tree_verify(target, cu_nodes, parents, tokens, accept_u, sample_u, max_
     """Accept a path of drafted tokens per sequence: target (and draft)
     [total_nodes, vocab] probabilities after each node, whose rows may be
     further apart than vocab (both alike); path_out [batch, max_nodes]."""
-    stride = _row_stride(target, "target")
-    for t, name, dt in ((cu_nodes, "cu_nodes", torch.int32), (parents, "parents", torch.int32),
-                        (tokens, "tokens", torch.int32), (accept_u, "accept_u", torch.float32),
-                        (sample_u, "sample_u", torch.float32), (n_path_out, "n_path_out", torch.int32),
-                        (next_token, "next_token", torch.int32)):
-        _need(t, (dt,), name, ndim=1)
-    _need(path_out, (torch.int32,), "path_out", ndim=2)
+    dev, stream = _here(target, "target", stream)
+    tp, row = _rows_at(target, dev, "target")
+    dp = None
+    if draft is not None:
+        dp, row_d = _rows_at(draft, dev, "draft")
+        if row_d != row or draft.shape != target.shape or draft.dtype is not target.dtype:
+            raise ValueError("draft must have target's type, shape and row stride")
     n, vocab = target.shape
     batch = cu_nodes.shape[0] - 1
-    if parents.shape[0] != n or tokens.shape[0] != n or accept_u.shape[0] != n:
+    if not parents.shape == tokens.shape == accept_u.shape == (n,):
         raise ValueError("parents, tokens and accept_u must have one value per row of target")
-    if sample_u.shape[0] != batch or n_path_out.shape[0] != batch or next_token.shape[0] != batch or \
-            tuple(path_out.shape) != (batch, max_nodes):
+    if not sample_u.shape == n_path_out.shape == next_token.shape == (batch,) or path_out.shape != (batch, max_nodes):
         raise ValueError("sample_u, n_path_out, next_token and path_out must have one row per sequence")
-    if draft is not None and (_row_stride(draft, "draft") != stride or draft.shape != target.shape or
-                              draft.dtype != target.dtype):
-        raise ValueError("draft must have target's type, shape and row stride")
-    code = {torch.float32: V4KV_FP32, torch.bfloat16: V4KV_BF16}
+    code = V4KV_FP32 if target.dtype is torch.float32 else V4KV_BF16
+    i32, f32 = torch.int32, torch.float32
     st = _lib.v4kv_tree_verify(
-        target.data_ptr(), code[target.dtype], _ptr(draft), code[draft.dtype] if draft is not None else 0,
-        vocab, stride, batch, cu_nodes.data_ptr(), n, max_nodes, parents.data_ptr(), tokens.data_ptr(),
-        accept_u.data_ptr(), sample_u.data_ptr(), path_out.data_ptr(), n_path_out.data_ptr(),
-        next_token.data_ptr(), _ptr(dev_status), _stream(stream))
-    _check("v4kv_tree_verify", st)
+        tp, code, dp, code, vocab, row, batch, _at(cu_nodes, i32, 1, dev, "cu_nodes"), n, max_nodes,
+        _at(parents, i32, 1, dev, "parents"), _at(tokens, i32, 1, dev, "tokens"),
+        _at(accept_u, f32, 1, dev, "accept_u"), _at(sample_u, f32, 1, dev, "sample_u"),
+        _at(path_out, i32, 2, dev, "path_out"), _at(n_path_out, i32, 1, dev, "n_path_out"),
+        _at(next_token, i32, 1, dev, "next_token"),
+        None if dev_status is None else _at(dev_status, i32, 1, dev, "dev_status"), stream)
+    if st != V4KV_OK:
+        raise V4KVError("v4kv_tree_verify", st)
 
 
 def v4kv_tree_gather(x, gate, cu_nodes, path, n_path, x_out, gate_out, cu_out, dev_status=None, stream=None):
     """Pack the accepted nodes' rows and gates ([total_nodes] or
     [total_nodes, dim]) for v4kv_compress_append (cu_out is its cu_seqlens)."""
-    _need(x, (torch.bfloat16,), "x", ndim=2)
-    _need(x_out, (torch.bfloat16,), "x_out", ndim=2)
-    _need(gate, (torch.float32,), "gate")
-    _need(gate_out, (torch.float32,), "gate_out")
-    _need(cu_nodes, (torch.int32,), "cu_nodes", ndim=1)
-    _need(path, (torch.int32,), "path", ndim=2)
-    _need(n_path, (torch.int32,), "n_path", ndim=1)
-    _need(cu_out, (torch.int32,), "cu_out", ndim=1)
-    dim = x.shape[1]
+    dev, stream = _here(x, "x", stream)
+    xp = _at(x, torch.bfloat16, 2, dev, "x")
+    nodes, dim = x.shape
     batch, max_nodes = path.shape
-    if x_out.shape[1] != dim or gate.dim() not in (1, 2) or gate_out.dim() != gate.dim() or \
-            gate.shape[0] != x.shape[0] or gate_out.shape[0] != x_out.shape[0] or \
-            (gate.dim() == 2 and (gate.shape[1] != dim or gate_out.shape[1] != dim)):
+    capacity = x_out.shape[0]
+    wide = gate.dim() == 2
+    if x_out.shape[1] != dim or gate.shape != ((nodes, dim) if wide else (nodes,)) or \
+            gate_out.shape != ((capacity, dim) if wide else (capacity,)):
         raise ValueError("gate must be [nodes] or [nodes, dim], and the outputs shaped like x and gate")
-    if n_path.shape[0] != batch or cu_nodes.shape[0] != batch + 1 or cu_out.shape[0] != batch + 1:
+    if n_path.shape != (batch,) or not cu_nodes.shape == cu_out.shape == (batch + 1,):
         raise ValueError("path and n_path need one row per sequence, cu_nodes and cu_out one value more")
-    st = _lib.v4kv_tree_gather(x.data_ptr(), gate.data_ptr(), dim, 1 if gate.dim() == 1 else dim, batch,
-                               cu_nodes.data_ptr(), x.shape[0], max_nodes, path.data_ptr(), n_path.data_ptr(),
-                               x_out.data_ptr(), gate_out.data_ptr(), x_out.shape[0], cu_out.data_ptr(),
-                               _ptr(dev_status), _stream(stream))
-    _check("v4kv_tree_gather", st)
+    i32, f32, gdim = torch.int32, torch.float32, 2 if wide else 1
+    st = _lib.v4kv_tree_gather(
+        xp, _at(gate, f32, gdim, dev, "gate"), dim, dim if wide else 1, batch,
+        _at(cu_nodes, i32, 1, dev, "cu_nodes"), nodes, max_nodes, _at(path, i32, 2, dev, "path"),
+        _at(n_path, i32, 1, dev, "n_path"), _at(x_out, torch.bfloat16, 2, dev, "x_out"),
+        _at(gate_out, f32, gdim, dev, "gate_out"), capacity, _at(cu_out, i32, 1, dev, "cu_out"),
+        None if dev_status is None else _at(dev_status, i32, 1, dev, "dev_status"), stream)
+    if st != V4KV_OK:
+        raise V4KVError("v4kv_tree_gather", st)
 
 
 def v4kv_kv_footprint_bytes(n_tokens, layer_ratios, dim, entry_bits, entry_scale_bytes=0,
