@@ -91,6 +91,7 @@ struct Bars {
   uint64_t kv_full[2][4];   // per stage and 128 dims
   uint64_t kv_empty[2][2];  // per stage and 256 dims
   uint64_t addr_full[kRing], addr_free[kRing];
+  uint64_t raw_full;        // bf16 entries have landed, to be split
   uint64_t ready, q_full, q_empty, s_full, s_free, p_full, pv_done, drain;
 };
 static_assert(sizeof(Bars) <= 320, "barrier area");
@@ -416,7 +417,7 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
   const TreeArgs& a = p.a;
   if (!t.entries) {
     const uint4 m4 = p.w.anc[x.node0];
-#pragma unroll
+#pragma unroll 1
     for (int r = 0; r < 4; ++r) {
       const int k = lane + 32 * r;
       int n = t.first + k;
@@ -448,6 +449,23 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
   }
   const PoolArgs& pool = a.main;
   const int32_t* bt = pool.block_table + (size_t)x.b * pool.max_blocks;
+  if (p.pages && t.first + kT <= x.n_all) {
+    // two whole pages: only their first rows' addresses are asked for
+    const int j = t.first + 64 * (lane >> 4);  // lanes 0 .. 15: the first page's items, 4 each
+    const int blk = j >> 6, pg = blk < pool.max_blocks ? bt[blk] : -1;
+    const bool there = pg >= 0 && pg < pool.num_pages;
+    if (!there && (lane & 15) == 0)
+      flag(a.dev_status, blk < pool.max_blocks ? V4KV_DEV_BAD_PAGE : V4KV_DEV_BAD_SLOT);
+    const size_t slot = (size_t)(there ? pg : 0) * 64;
+    if ((lane & 15) == 0)
+      rows[64 * (lane >> 4)] = there ? reinterpret_cast<unsigned long long>(pool.data) + slot * kD : 0;
+    const float4 s4 = *reinterpret_cast<const float4*>(pool.scales + slot + 4 * (lane & 15));
+    meta[4 * lane] = item_meta(s4.x, there);
+    meta[4 * lane + 1] = item_meta(s4.y, there);
+    meta[4 * lane + 2] = item_meta(s4.z, there);
+    meta[4 * lane + 3] = item_meta(s4.w, there);
+    return;
+  }
   int j[4], pg[4], err = 0;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -526,12 +544,12 @@ __device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& l
   return scale_down(m);
 }
 
-// The rows' lanes' 32 bytes of bf16 that were copied to where the lane's two
-// terms go: split in place, `n` rows from r0 on.
-__device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, int n, int lane, uint8_t* hi_dst,
+// Eight rows from r0 on whose 32 bytes of bf16 a lane were copied to where the
+// lane's two terms go: split in place.
+__device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
                                         uint8_t* lo_dst, float4* meta) {
-#pragma unroll 2
-  for (int r = r0; r < r0 + n; ++r) {
+#pragma unroll 1
+  for (int r = r0; r < r0 + 8; ++r) {
     const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r, lane & 7);
     uint4 raw[2], hi, lo;
     raw[0] = *reinterpret_cast<uint4*>(hi_dst + off);
@@ -544,6 +562,42 @@ __device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, 
 }
 
 // ------------------------------------------------------------------ the sweep
+
+// O^T's columns of a warp's 16 rows times the rows' factors
+__device__ __noinline__ void scale_rows(uint32_t o, const float* fac) {
+#pragma unroll 1
+  for (int g = 0; g < 8; ++g) {
+    const uint32_t at = o + kR * (g >> 1) + 8 * (g & 1);
+    uint32_t r8[8];
+    tmem_ld8(at, r8);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) r8[n] = __float_as_uint(__uint_as_float(r8[n]) * fac[8 * (g & 1) + n]);
+    tmem_st8(at, r8);
+  }
+}
+
+__device__ __noinline__ uint32_t rows_seeing(uint32_t seen, const Unit& x, bool entries, int r0, int row,
+                                             const int4* vis, const uint4* anc) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + 8 * j;
+#pragma unroll 1
+    for (int m = 0; m < 4; ++m) {
+      bool v;
+      if (entries) {
+        v = r < vis[row + m].x;
+      } else if (r < x.n_win) {
+        v = x.w0 + r >= vis[row + m].y;
+      } else {
+        const int k = min(r - x.n_win, V4KV_MAX_TREE_NODES - 1);
+        v = (reinterpret_cast<const uint32_t*>(anc + m)[k >> 5] >> (k & 31)) & 1;
+      }
+      if (!v) seen &= ~(1u << (4 * j + m));
+    }
+  }
+  return seen;
+}
 
 }  // namespace
 
@@ -568,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       tc::mbar_init(&bars->addr_full[s], 32);
       tc::mbar_init(&bars->addr_free[s], 1);
     }
+    tc::mbar_init(&bars->raw_full, 4);
     tc::mbar_init(&bars->ready, 4);
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 1);
@@ -675,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             // a page that is missing is read behind the pool's end: zeros
             y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
                                 : a.main.num_pages * a.main.spb;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             if ((c & 1) == 0) ok = __all_sync(0xffffffffu, ok && wait_empty(im, c >> 1));
             if (!ok) break;
@@ -733,12 +788,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             }
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
-          if (t.images == 2 && t.entries)
-            split_rows(rows, 32 * w, 32, lane, dst, sm + kVOff + (s ^ 1) * kStage, mt);
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane < 4)
+          if (t.images == 2 && t.entries) {  // the softmax warps, idle now, split them
+            if (lane == 0) tc::mbar_arrive(&bars->raw_full);
+          } else if (lane < 4) {
             for (int k = 0; k < t.images; ++k) tc::mbar_arrive(&bars->kv_full[(im + k) & 1][lane]);
+          }
         }
         im += t.images;
         ++done;
@@ -774,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         const uint32_t s = (m + k) & 1;
         const uint64_t vk = v_k + (uint64_t)(s * (kStage >> 4));
         const uint32_t sfa = tmem + (k ? kLow : kOne);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           wait_all(&bars->kv_full[s][c], ((m + k) >> 1) & 1);
           if (!ok) break;
@@ -845,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
             const uint32_t s = (im + k) & 1;
             const uint64_t vm = v_m + (uint64_t)(s * (kStage >> 4));
             const uint32_t sfa = tmem + (k ? kLow : kOne);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -919,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
     if (w == 0 && lane < 2 && !(qd & 1)) raise[lane] = 0;
     bool ok = true, seg_open = true, any = false;
     int seg_tile0 = 0;
-    uint32_t im = 0, done = 0, seg = 0;
+    uint32_t im = 0, done = 0, seg = 0, split = 0;
     float l[4], fa[4], ref[4];
     for (int i = 0; i < n_tiles; ++i) {
       if (seg_open) {
@@ -948,6 +1004,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       const Tile t = tile_of(p, x);
       const bool seg_last = x.tile + 1 == x.te + x.tr || i + 1 == n_tiles;
       if (t.count > 0) {
+        if (t.images == 2 && t.entries) {
+          // bf16 entries: eight rows a warp
+          ok = tc::mbar_wait(&bars->raw_full, split & 1, abort_flag);
+          if (named_or(bar, !ok)) {
+            ok = false;
+            break;
+          }
+          ++split;
+          const uint32_t slot = done % kRing, s = im & 1;
+          split_rows(reinterpret_cast<const unsigned long long*>(sm + kPtrOff) + slot * kT, 8 * warp, lane,
+                     sm + kVOff + s * kStage, sm + kVOff + (s ^ 1) * kStage, meta + slot * kT);
+          tc::fence_proxy_async_smem();
+          named_sync(bar);
+          if (w == 0 && lane < 8) tc::mbar_arrive(&bars->kv_full[lane >> 2][lane & 3]);
+        }
         ok = tc::mbar_wait(&bars->s_full, done & 1, abort_flag);
         tc::tc_fence_after();
         // the items' {scale, log2 |scale|, 1 / |scale|} and the scores u[j][m],
@@ -989,23 +1060,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->s_free);
         if (!p.per_node && (!t.entries || t.first + kT > x.n_all)) {
-#pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            const int r = t.first + 32 * w + (lane >> 2) + 8 * j;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              bool v;
-              if (t.entries) {
-                v = r < vis[row_t + m].x;
-              } else if (r < x.n_win) {
-                v = x.w0 + r >= vis[row_t + m].y;
-              } else {
-                const int k = min(r - x.n_win, V4KV_MAX_TREE_NODES - 1);
-                v = (reinterpret_cast<const uint32_t*>(anc + m)[k >> 5] >> (k & 31)) & 1;
-              }
-              if (!v) seen &= ~(1u << (4 * j + m));
-            }
-          }
+          const Unit y = x;
+          seen = rows_seeing(seen, y, t.entries, t.first + 32 * w + (lane >> 2), row_t, vis, anc);
         }
         if (seen != 0xffffu) {
 #pragma unroll
@@ -1116,19 +1172,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           }
           put_scales();
           named_sync(bar);
-          if (any) {
-#pragma unroll 1
-            for (int g = 0; g < 8; ++g) {
-              const int r0 = 16 * qd + 8 * (g & 1);
-              const uint32_t at = lanes + kOCol + kR * (g >> 1) + r0;
-              uint32_t r8[8];
-              tmem_ld8(at, r8);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int n = 0; n < 8; ++n) r8[n] = __float_as_uint(__uint_as_float(r8[n]) * fac[r0 + n]);
-              tmem_st8(at, r8);
-            }
-          }
+          if (any) scale_rows(lanes + kOCol + 16 * qd, fac + 16 * qd);
         }
         any = true;
         // the two quarters write the hi and the lo terms' scales of the half
@@ -1238,17 +1282,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
 // block c joins the unit that its range begins inside, if it is the first to
 // begin there.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ Params p) {
-  tc::pdl_wait();
+  // What the prep kernel wrote is read before the wait: the sweep launched this
+  // grid after its own wait for that kernel.
   tc::pdl_launch_dependents();
   const int c = blockIdx.x;
   const int4 rec = p.w.rec[c];
   const int begin = rec.x - rec.w;  // the unit's first tile
-  if (c == 0 || rec.w == 0 || p.w.rec[c - 1].x > begin) return;
+  if (c == 0 || rec.w == 0 || p.w.rec[max(c - 1, 0)].x > begin) {
+    tc::pdl_wait();
+    return;
+  }
   const TreeArgs& a = p.a;
   Unit x;
   unit_load(p, x, rec.y);
   const int end = begin + x.te + x.tr;
   const int row = 8 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  tc::pdl_wait();
   if (row >= x.nrows) return;
   float acc[16], m = kNone, l = 0.f;
 #pragma unroll
@@ -1576,7 +1625,8 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.heads, a.total_nodes, a.topk ? a.k : 0, a.window_len,
          a.max_len, p.grid);
   cudaError_t e = cudaSuccess;
-  p.pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64;
+  p.pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64 &&
+            (reinterpret_cast<uintptr_t>(a.main.scales) & 15) == 0;  // (their scales are read by fours)
   if (p.pages) {
     e = encode_cols_u8(&p.map, a.main.data, (uint64_t)a.main.num_pages * a.main.spb, kD, 128, 64);
     if (e != cudaSuccess) return e;
