@@ -435,7 +435,8 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
   st = check_device(&sms);
   if (st != V4KV_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < tree_workspace_bytes(batch, heads, total_nodes, topk ? k : 0, window_len, max_seq_len, sms))
+      workspace_bytes < tree_workspace_bytes(batch, heads, total_nodes, max_nodes, topk ? k : 0, window_len,
+                                             max_seq_len, ratio, main_cache->dtype, sms))
     return V4KV_ERR_INVALID_ARG;
   if (empty) return V4KV_OK;
   TreeArgs a{};
@@ -466,7 +467,6 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
 v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total_nodes,
                                      int32_t max_nodes, int32_t max_seq_len, int32_t ratio,
                                      int32_t window_len, int32_t k, int32_t main_dtype, size_t* bytes) {
-  (void)main_dtype;
   if (!bytes || batch <= 0 || total_nodes < 0 || max_seq_len < 0 || k < 0) return V4KV_ERR_INVALID_ARG;
   if (max_nodes < 1 || max_nodes > V4KV_MAX_TREE_NODES || window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
   if (heads < 1 || heads > 128) return V4KV_ERR_UNSUPPORTED;
@@ -474,7 +474,8 @@ v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total
   int sms = 0;
   v4kv_status st = check_device(&sms);
   if (st != V4KV_OK) return st;
-  *bytes = tree_workspace_bytes(batch, heads, total_nodes, k, window_len, max_seq_len, sms);
+  *bytes = tree_workspace_bytes(batch, heads, total_nodes, max_nodes, k, window_len, max_seq_len, ratio, main_dtype,
+                                sms);
   return V4KV_OK;
 }
 

@@ -203,8 +203,8 @@ struct GatherArgs {
 };
 
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
-size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int k, int window_len, int max_len,
-                            int num_sms);
+size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len,
+                            int ratio, int main_dtype, int num_sms);
 cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_tree_gather(const GatherArgs& a, cudaStream_t stream);
 

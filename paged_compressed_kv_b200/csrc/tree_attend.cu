@@ -57,6 +57,7 @@ constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr float kRaise = 40.f;   // log2 by which a score may pass its reference
 constexpr int kPairs = 256;     // rotated pairs of a row at most
 constexpr int kPrepRows = 4;    // rows a warp of the prep kernel splits
+constexpr int kStageRows = 8;   // entries it copies
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr uint32_t kQOff = 0;                 // 4 x [128 rows (64 hi, 64 lo) x 128 dims]
@@ -106,6 +107,8 @@ struct TreeWs {
   int4* units;        // [images][4] Unit's fields
   uint8_t* raw;       // rows of the windows and trees as two e4m3 terms, 512 bytes each
   float2* raw_meta;   // their {scale, 0 or -inf: no such row}
+  uint8_t* ent;       // entries gathered from pages of two (staged), 512 bytes each
+  float4* ent_meta;   // their item_meta
   long long* cost;    // [batch + 1] prefix sums over sequences
   int32_t* tiles;     // [batch + 1]
   int4* rec;          // [grid + 1] a block's first tile: {index, its unit, -, tile in that}
@@ -122,8 +125,11 @@ struct Params {
   int per_node;  // a unit's rows belong to one node
   int raw_blocks;  // prep blocks per sequence for its raw rows
   int max_units;   // units of a sequence at most
-  int pages;     // tiles of entries are whole pages of 64 rows, loaded by TMA
-  CUtensorMap map;  // boxes of 64 rows x 128 bytes of main_cache
+  int boxes;     // tiles of entries that every node sees are loaded by TMA
+  int staged;    // entries of a sequence in w.ent, 0: the boxes are pages
+  const uint8_t* box_data;  // what they are taken from, and its rows
+  int box_rows;
+  CUtensorMap map;  // boxes of 64 rows x 128 bytes of box_data
 };
 
 __device__ __forceinline__ int seq_len(const TreeArgs& a, int b) {
@@ -258,6 +264,14 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const Unit& x) {
   t.count = min(kT, (t.entries ? x.n_ent : x.n_win + x.n_tree) - t.first);
   t.images = t.entries && p.a.main.dtype == V4KV_FP8_E4M3 ? 1 : 2;
   return t;
+}
+
+// entries that every node of a sequence sees
+__device__ __forceinline__ int seen_by_all(const Params& p, int L) {
+  return max(0, L + 1 - p.a.window_len) >> p.ratio_log;
+}
+__device__ __forceinline__ bool box_tile(const Params& p, const Unit& x, const Tile& t) {
+  return p.boxes && t.entries && t.first + kT <= seen_by_all(p, x.L);
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -397,7 +411,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
-// ------------------------------------------------------------------ loading (warps 8-11)
+// ------------------------------------------------------------------ loading
 
 // what the softmax needs of an item: its scale, and for the weight of its raw
 // codes log2 |scale| and 1 / |scale|. A zero scale stands for zero codes (the
@@ -449,7 +463,14 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
   }
   const PoolArgs& pool = a.main;
   const int32_t* bt = pool.block_table + (size_t)x.b * pool.max_blocks;
-  if (p.pages && t.first + kT <= x.n_all) {
+  if (box_tile(p, x, t)) {
+    if (p.staged) {
+      const size_t row = (size_t)x.b * p.staged + t.first;
+      if (lane < 2) rows[64 * lane] = reinterpret_cast<unsigned long long>(p.w.ent) + (row + 64 * lane) * kD;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) meta[lane + 32 * r] = p.w.ent_meta[row + lane + 32 * r];
+      return;
+    }
     // two whole pages: only their first rows' addresses are asked for
     const int j = t.first + 64 * (lane >> 4);  // lanes 0 .. 15: the first page's items, 4 each
     const int blk = j >> 6, pg = blk < pool.max_blocks ? bt[blk] : -1;
@@ -637,6 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
   if (warp == 20) tc::tmem_alloc(tmem_slot, kCols);
   tc::pdl_wait();
   tc::pdl_launch_dependents();
+  // what the prep kernel stored is read by bulk copies
+  asm volatile("fence.proxy.async.global;" ::: "memory");
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -720,16 +743,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         const uint32_t s = im & 1, slot = done % kRing;
         const unsigned long long* rows = reinterpret_cast<const unsigned long long*>(sm + kPtrOff) + slot * kT;
         ok = tc::mbar_wait(&bars->addr_full[slot], (done / kRing) & 1, abort_flag);
-        if (t.images == 1 && p.pages && t.first + kT <= x.n_all) {
-          // two whole pages, every row of them visible: two boxes per 128 dims,
+        if (box_tile(p, x, t)) {
+          // 2 x 64 rows in order, every one visible: two boxes per 128 dims,
           // as the last tile's product leaves them. All four warps wait and
           // arrive, so that none falls a phase behind.
           int y[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             // a page that is missing is read behind the pool's end: zeros
-            y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(a.main.data)) / kD)
-                                : a.main.num_pages * a.main.spb;
+            y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(p.box_data)) / kD)
+                                : p.box_rows;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             if ((c & 1) == 0) ok = __all_sync(0xffffffffu, ok && wait_empty(im, c >> 1));
@@ -1391,7 +1414,36 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     }
     return;
   }
-  const int raw_end = a.batch + 1 + a.batch * p.raw_blocks;
+  const int raw_end = a.batch + 1 + a.batch * p.raw_blocks, q_end = raw_end + 2 * a.batch * p.max_units;
+  if (b >= q_end) {
+    // kStageRows entries a warp, of the whole tiles that every node sees
+    const int per = p.staged / (8 * kStageRows), bb = (b - q_end) / per;
+    const int j0 = ((b - q_end) % per * 8 + warp) * kStageRows;
+    const int L = seq_len(a, bb);
+    if (j0 >= seen_by_all(p, L) / kT * kT) return;
+    const TreeSeq s = tree_seq(a.cu_nodes, bb, a.total_nodes, a.max_nodes, nullptr);
+    if (s.n == 0) return;
+    const size_t row = (size_t)bb * p.staged + j0;
+    const PoolArgs& pool = a.main;
+    int slot = -1;
+    if (lane < kStageRows) {
+      const int pg = page_of(pool.block_table + (size_t)bb * pool.max_blocks, pool.max_blocks, j0 + lane, pool.spb,
+                             pool.num_pages, a.dev_status);
+      if (pg >= 0) slot = pg * pool.spb + (j0 + lane) % pool.spb;
+      p.w.ent_meta[row + lane] = item_meta(pg >= 0 ? pool.scales[slot] : 0.f, pg >= 0);
+    }
+    uint4 v[kStageRows];
+#pragma unroll
+    for (int k = 0; k < kStageRows; ++k) {
+      const int at = __shfl_sync(0xffffffffu, slot, k);
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (at >= 0) v[k] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool.data) + (size_t)at * kD)[lane];
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.w.ent + row * kD) + lane;
+#pragma unroll
+    for (int k = 0; k < kStageRows; ++k) dst[k * (kD / 16)] = v[k];
+    return;
+  }
   if (b >= raw_end) {
     // half a unit's Q: row 4 c + 2 k + e of a quarter at row 8 k + 2 c + e of it
     // (hi terms) and 64 rows on (lo terms)
@@ -1573,10 +1625,28 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
 
 namespace {
 
+int units_per_seq(int heads, int max_nodes, int k) {
+  return heads % kR == 0 || k > 0 ? max_nodes * ((heads + kR - 1) / kR) : (max_nodes * heads + kR - 1) / kR;
+}
+
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Entries per sequence that the prep kernel copies to consecutive rows, in whole
+// tiles, or 0. At ratio 128 a page has two entries, and a tile's 128 rows come
+// by 16-byte asynchronous copies, 6100 cycles against 3200 of products; copied
+// once, they come by TMA boxes as pages of 64 do. Every unit of a sequence reads
+// them again, so the copy has to be shared: with 32 sequences of 128K to 1M
+// tokens it gives 382 us against 428 for 16 units each, but 132 against 129 for
+// four and 74 against 57 for one.
+int staged_rows(int batch, int heads, int max_nodes, int k, int window_len, int max_len, int ratio, int main_dtype) {
+  if (ratio != 128 || k > 0 || main_dtype != V4KV_FP8_E4M3) return 0;
+  if (units_per_seq(heads, max_nodes, k) < 6) return 0;
+  const long long n = max(0, max_len + 1 - window_len) / ratio / kT * kT;
+  return batch * n < (1LL << 30) ? (int)n : 0;
+}
+
 size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, int k, int window_len,
-              int max_len, int grid) {
+              int max_len, int grid, int staged) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = base ? base + at : nullptr;
@@ -1596,6 +1666,8 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
   const size_t raws = (size_t)batch * (window_len - 1 < max_len ? window_len - 1 : max_len) + total_nodes;
   x.raw = take(raws * 2 * kD);
   x.raw_meta = reinterpret_cast<float2*>(take(raws * sizeof(float2)));
+  x.ent = take((size_t)batch * staged * kD);
+  x.ent_meta = reinterpret_cast<float4*>(take((size_t)batch * staged * sizeof(float4)));
   x.cost = reinterpret_cast<long long*>(take(((size_t)batch + 1) * 8));
   x.tiles = reinterpret_cast<int32_t*>(take(((size_t)batch + 1) * 4));
   x.rec = reinterpret_cast<int4*>(take(((size_t)grid + 1) * sizeof(int4)));
@@ -1607,9 +1679,10 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
 
 }  // namespace
 
-size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int k, int window_len, int max_len,
-                            int num_sms) {
-  return layout(nullptr, nullptr, batch, heads, total_nodes, k, window_len, max_len, num_sms);
+size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len,
+                            int ratio, int main_dtype, int num_sms) {
+  return layout(nullptr, nullptr, batch, heads, total_nodes, k, window_len, max_len, num_sms,
+                staged_rows(batch, heads, max_nodes, k, window_len, max_len, ratio, main_dtype));
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream) {
@@ -1618,23 +1691,28 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   p.grid = num_sms;
   p.per_node = a.topk != nullptr || a.heads % kR == 0;
   p.hc = (a.heads + kR - 1) / kR;
-  p.max_units = p.per_node ? a.max_nodes * p.hc : (a.max_nodes * a.heads + kR - 1) / kR;
+  p.max_units = units_per_seq(a.heads, a.max_nodes, a.topk ? a.k : 0);
   p.ratio_log = a.ratio == 4 ? 2 : 7;
   p.spb_log = 8 - p.ratio_log;
   p.raw_blocks = (min(a.window_len - 1, a.max_len) + a.max_nodes + 8 * kPrepRows - 1) / (8 * kPrepRows);
+  p.staged = staged_rows(a.batch, a.heads, a.max_nodes, a.topk ? a.k : 0, a.window_len, a.max_len, a.ratio, a.main.dtype);
   layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.heads, a.total_nodes, a.topk ? a.k : 0, a.window_len,
-         a.max_len, p.grid);
+         a.max_len, p.grid, p.staged);
   cudaError_t e = cudaSuccess;
-  p.pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64 &&
-            (reinterpret_cast<uintptr_t>(a.main.scales) & 15) == 0;  // (their scales are read by fours)
-  if (p.pages) {
-    e = encode_cols_u8(&p.map, a.main.data, (uint64_t)a.main.num_pages * a.main.spb, kD, 128, 64);
+  const bool pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64 &&
+                     (long long)a.main.num_pages * 64 < (1LL << 30) &&
+                     (reinterpret_cast<uintptr_t>(a.main.scales) & 15) == 0;  // (their scales are read by fours)
+  p.boxes = pages || p.staged > 0;
+  if (p.boxes) {
+    p.box_data = p.staged ? p.w.ent : static_cast<const uint8_t*>(a.main.data);
+    p.box_rows = p.staged ? a.batch * p.staged : a.main.num_pages * 64;
+    e = encode_cols_u8(&p.map, p.box_data, (uint64_t)p.box_rows, kD, 128, 64);
     if (e != cudaSuccess) return e;
   }
   e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1 + a.batch * (p.raw_blocks + 2 * p.max_units)), dim3(256), 0, stream, p);
+  e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1 + a.batch * (p.raw_blocks + 2 * p.max_units + p.staged / (8 * kStageRows))), dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_attend_kernel, dim3(p.grid), dim3(kThreads), kSmemBytes, stream, p);
   if (e != cudaSuccess) return e;

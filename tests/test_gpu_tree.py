@@ -329,6 +329,88 @@ def test_bad_inputs_are_flagged_and_skipped():
     c.check(d["out"])
 
 
+def without(c, b, i, missing):
+    """The oracle for a node whose entries on a page are left out."""
+    lo = c.cu[b]
+    depth = len(tree.family(c.parents[lo:c.cu[b + 1]], i)) - 1
+    spb = 256 // c.ratio
+    seen = np.arange(max(0, c.lens[b] + depth + 1 - c.W) // c.ratio)
+    row = seen[seen // spb != missing].astype(np.int32)
+    return tree.attend_node(c.q[lo + i], i, c.parents[lo:c.cu[b + 1]], c.k_tree[lo:c.cu[b + 1]], c.main.seq(b),
+                            c.win.seq(b), c.lens[b], c.ratio, c.W, 1 / math.sqrt(512), topk_row=row)
+
+
+@pytest.mark.parametrize("lens,counts,ratio,missing", [
+    ([70000, 33000, 16600], [8, 3, 1], 128, 100),  # in a tile that every node sees
+    ([70000, 33000, 16600], [8, 3, 1], 128, 272),  # in the last one
+    ([70000, 33000, 16600], [2, 3, 1], 128, 100),
+    ([3000, 700, 140], [8, 3, 1], 4, 3),
+    ([3000, 700, 140], [8, 3, 1], 4, 11),
+])
+def test_missing_pages_and_scales_of_any_value(lens, counts, ratio, missing):
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(874 + missing, lens, counts, 64, ratio=ratio)
+    r = synth.rng(10)
+    c.main.scales[:] *= np.exp2(r.integers(-12, 4, c.main.scales.shape)).astype(np.float32)
+    c.main.scales[r.random(c.main.scales.shape) < 0.1] = 0.0
+    c.main.scales[r.random(c.main.scales.shape) < 0.2] *= -1.0
+    d = c.device()
+    c.run(d)
+    assert int(d["st"].item()) == 0
+    c.check(d["out"])
+    clean = d["out"].clone()
+    d["main"].block_table[0, missing] = 10 ** 6
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_PAGE
+    n = counts[0]
+    assert torch.equal(d["out"][n:], clean[n:])
+    out = d["out"].float().cpu().numpy().astype(np.float64)
+    for i in range(n):
+        ref, mass = without(c, 0, i, missing)
+        tol = (2.0 ** -9 + 2.0 ** -11) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max()
+        assert (np.abs(out[i] - ref) <= tol).all()
+
+
+def test_scales_at_any_address():
+    """Entry scales that begin 4, 8 and 12 bytes behind a 16-byte boundary."""
+    c = TreeCase(876, [3000, 517], [5, 3], 64)
+    d = c.device()
+    c.run(d)
+    c.check(d["out"])
+    flat = d["main"].scales.reshape(-1)
+    for off in (1, 2, 3):
+        room = torch.full((flat.numel() + 4,), float("nan"), device="cuda")
+        room[off:off + flat.numel()] = flat
+        d["main"].scales = room[off:off + flat.numel()].view_as(d["main"].scales)
+        d["out"].fill_(7.0)
+        c.run(d)
+        c.check(d["out"])
+    assert int(d["st"].item()) == 0
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different sequences with one workspace, replayed in turn."""
+    c, e = TreeCase(877, [2000, 300], [6, 2], 64), TreeCase(878, [17000], [8], 64, ratio=128)
+    d, f = c.device(), e.device()
+    f["ws"] = d["ws"] = d["ws"] if d["ws"].numel() > f["ws"].numel() else f["ws"]
+    c.run(d)
+    ref = d["out"].clone()
+    e.run(f)
+    ref2 = f["out"].clone()
+    graphs = []
+    for case, dev in ((c, d), (e, f)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            case.run(dev)
+    for _ in range(3):
+        d["out"].fill_(0)
+        f["out"].fill_(0)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d["out"], ref) and torch.equal(f["out"], ref2)
+
+
 def test_host_refusals_that_need_a_device():
     from paged_compressed_kv_b200 import v4kv
     c = TreeCase(872, [300], [2], 64)
