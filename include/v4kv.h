@@ -376,6 +376,8 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  *               nodes are rows cu_nodes[b] .. cu_nodes[b+1] of every per-node
  *               array (rows behind cu_nodes[batch] are neither read nor written)
  *   total_nodes host: rows of the per-node arrays
+ *               (v4kv_tree_attention flags cu_nodes that decrease with
+ *               V4KV_DEV_OVERFLOW and leaves out as it was)
  *   max_nodes   host bound of a sequence's nodes, 1 .. V4KV_MAX_TREE_NODES; the
  *               nodes of a longer sequence beyond it are left out and flagged
  *               V4KV_DEV_OVERFLOW
@@ -415,6 +417,9 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  *   out         device bf16 [total_nodes, heads, dim]
  *   workspace   device scratch of v4kv_tree_workspace_size bytes, 256-byte
  *               aligned; contents need not be initialised
+ * Sizes whose rows or tiles of 128 items do not count in 31 bits are refused
+ * with V4KV_ERR_UNSUPPORTED. max_seq_len sets the work that may be planned and,
+ * at ratio 128, up to 4.2 bytes of workspace per token and sequence.
  * Everything else, and a node with nothing to attend to (zeros), is as in
  * v4kv_decode_attention.
  */

@@ -60,6 +60,9 @@ def verify(target, draft, parents, tokens, accept_u, sample_u):
     """(path, next token) of one sequence: target and draft [n, V] (draft None
     for fixed guesses), fp64 arithmetic on the given values."""
     target = np.asarray(target, dtype=np.float64)
+    if draft is not None:
+        draft = np.asarray(draft, dtype=np.float64)
+        draft = np.where(draft > 0, draft, 0.0)
     n, vocab = target.shape
     now, path = 0, [0]
     while True:
@@ -77,7 +80,7 @@ def verify(target, draft, parents, tokens, accept_u, sample_u):
                 total -= rest[x]
                 rest[x] = 0.0
             else:
-                rest = np.maximum(rest - total * np.asarray(draft[now], dtype=np.float64), 0.0)
+                rest = np.maximum(rest - total * draft[now], 0.0)
                 total = rest.sum()
         if accepted is None:
             break

@@ -420,10 +420,12 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
                                 int32_t* dev_status, void* stream) {
   if (!tree_ok(batch, cu_nodes, total_nodes, max_nodes)) return V4KV_ERR_INVALID_ARG;
   if (total_nodes > 0 && (!parents || !k_tree || !aligned16(k_tree))) return V4KV_ERR_INVALID_ARG;
-  if ((long long)total_nodes * heads > 0x7fffffffLL || (long long)batch * window_len + total_nodes > 0x7fffffffLL)
-    return V4KV_ERR_UNSUPPORTED;
   // no drafted token may leave the window: the entries it would belong to do not exist
   if (window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
+  const bool sizes = max_seq_len >= 0 && heads >= 1 && heads <= 128 && (ratio == 4 || ratio == 128) &&
+                     (!topk || (k >= 1 && k <= 2048));
+  if (sizes && !tree_sizes_ok(batch, heads, total_nodes, max_nodes, topk ? k : 0, window_len, max_seq_len, ratio))
+    return V4KV_ERR_UNSUPPORTED;
   // the other arguments are checked as v4kv_decode_attention checks them (the
   // per-node arrays of an empty call may be NULL)
   const bool empty = total_nodes == 0;
@@ -456,7 +458,7 @@ v4kv_status v4kv_tree_attention(const void* q, int32_t q_dtype, int32_t batch, i
   a.heads = heads;
   a.total_nodes = total_nodes;
   a.max_nodes = max_nodes;
-  a.max_len = max_seq_len;
+  a.max_len = min(max_seq_len, 0x7fffffff - 256);  // positions are 32-bit
   a.ratio = ratio;
   a.window_len = window_len;
   a.k = topk ? k : 0;
@@ -470,7 +472,9 @@ v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total
   if (!bytes || batch <= 0 || total_nodes < 0 || max_seq_len < 0 || k < 0) return V4KV_ERR_INVALID_ARG;
   if (max_nodes < 1 || max_nodes > V4KV_MAX_TREE_NODES || window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
   if (heads < 1 || heads > 128) return V4KV_ERR_UNSUPPORTED;
-  if (ratio != 4 && ratio != 128) return V4KV_ERR_INVALID_ARG;
+  if ((ratio != 4 && ratio != 128) || k > 2048) return V4KV_ERR_INVALID_ARG;
+  if (!tree_sizes_ok(batch, heads, total_nodes, max_nodes, k, window_len, max_seq_len, ratio))
+    return V4KV_ERR_UNSUPPORTED;
   int sms = 0;
   v4kv_status st = check_device(&sms);
   if (st != V4KV_OK) return st;

@@ -203,6 +203,8 @@ struct GatherArgs {
 };
 
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
+// whether rows, tiles and blocks of a call can be counted in 31 bits
+bool tree_sizes_ok(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len, int ratio);
 size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len,
                             int ratio, int main_dtype, int num_sms);
 cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);

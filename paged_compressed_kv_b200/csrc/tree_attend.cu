@@ -1564,12 +1564,14 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
   __shared__ int tsum[8];
   long long ccarry = 0;
   int tcarry = 0;
+  bool falls = false;
   for (int base = 0; base < a.batch; base += 256) {
     const int bb = base + t;
     long long cost = 0;
     int tiles = 0;
     if (bb < a.batch) {
       const SeqPlan q = plan_of(p, bb, nullptr);
+      falls |= a.cu_nodes[bb] > a.cu_nodes[bb + 1];
       cost = (long long)q.units * unit_cost(p, q);
       tiles = q.units * (q.te + q.tr);
     }
@@ -1603,6 +1605,9 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     }
     __syncthreads();
   }
+  // Sequences that share rows share the workspace's records of them: nothing runs
+  // (the sequences with a negative count have been flagged).
+  if (__syncthreads_or(falls)) tcarry = 0;
   const int blocks = min(p.grid, tcarry);
   for (int c = t; c <= p.grid; c += 256) {
     int4 rec = make_int4(tcarry, 0, 0, 0);
@@ -1641,8 +1646,8 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int staged_rows(int batch, int heads, int max_nodes, int k, int window_len, int max_len, int ratio, int main_dtype) {
   if (ratio != 128 || k > 0 || main_dtype != V4KV_FP8_E4M3) return 0;
   if (units_per_seq(heads, max_nodes, k) < 6) return 0;
-  const long long n = max(0, max_len + 1 - window_len) / ratio / kT * kT;
-  return batch * n < (1LL << 30) ? (int)n : 0;
+  const long long n = max(0LL, max_len + 1LL - window_len) / ratio / kT * kT;
+  return batch * n <= (1LL << 21) ? (int)n : 0;  // at most 1.1 GB
 }
 
 size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, int k, int window_len,
@@ -1678,6 +1683,19 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
 }
 
 }  // namespace
+
+bool tree_sizes_ok(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len, int ratio) {
+  const long long most = 0x7fffffffLL, per = (heads + kR - 1) / kR;
+  if ((long long)total_nodes * heads > most) return false;
+  if ((long long)batch * (window_len - 1 < max_len ? window_len - 1 : max_len) + total_nodes > most) return false;
+  // tiles of all units, and blocks of the prep kernel
+  const long long units = heads % kR == 0 || k > 0 ? total_nodes * per : (long long)total_nodes * heads / kR + batch + 1;
+  const long long te = ((k > 0 ? k : max(0LL, (long long)max_len + max_nodes - window_len) / ratio) + kT - 1) / kT;
+  const long long raw = min((long long)max_len, window_len - 1LL) + max_nodes;
+  if (units * (te + (raw + kT - 1) / kT) > most) return false;
+  return batch * (2 + raw / (8 * kPrepRows) + 1 + 2LL * units_per_seq(heads, max_nodes, k)) +
+             (1LL << 21) / (8 * kStageRows) < most;
+}
 
 size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len,
                             int ratio, int main_dtype, int num_sms) {

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kVThreads, 2)
     sh.parent[tid] = ok ? parent : -1;  // a child that cannot be accepted is never asked
     sh.token[tid] = x;
     sh.p[tid] = p;
-    sh.q[tid] = q;
+    sh.q[tid] = fmaxf(q, 0.f);  // NaN too
     sh.u[tid] = a.accept_u[s.first + tid];
   }
   if (tid == 0) {

@@ -418,6 +418,15 @@ def _at(t, dtype, ndim, dev, what):
     raise ValueError(f"{what} must be on the current device")
 
 
+def _pool_at(pool, dev, what):
+    """A pool's descriptor, all of it on the current device."""
+    c = pool.c()
+    if pool.data.get_device() != dev or pool.block_table.get_device() != dev or \
+            (pool.scales is not None and pool.scales.get_device() != dev):
+        raise ValueError(f"{what} must be on the current device")
+    return c
+
+
 def v4kv_tree_attention(q, cu_nodes, parents, k_tree, main, window, seq_lens, max_nodes, max_seq_len, ratio,
                         window_len, out, workspace, topk=None, sm_scale=None, rope=None, dev_status=None,
                         stream=None):
@@ -438,7 +447,9 @@ def v4kv_tree_attention(q, cu_nodes, parents, k_tree, main, window, seq_lens, ma
     if topk is not None and topk.shape[0] != n:
         raise ValueError("topk must have one row per node")
     rope = rope or Rope()
-    mc, wc = main.c(), window.c()
+    mc, wc = _pool_at(main, dev, "main"), _pool_at(window, dev, "window")
+    if main.block_table.shape[0] < batch or window.block_table.shape[0] < batch:
+        raise ValueError("the block tables must have one row per sequence")
     st = _lib.v4kv_tree_attention(
         qp, V4KV_FP32 if fp32 else V4KV_BF16, batch, heads, _at(cu_nodes, torch.int32, 1, dev, "cu_nodes"), n,
         max_nodes, _at(parents, torch.int32, 1, dev, "parents"), _at(k_tree, torch.bfloat16, 2, dev, "k_tree"),

@@ -316,6 +316,13 @@ def test_bad_inputs_are_flagged_and_skipped():
     c.run(d)
     assert int(d["st"].item()) & v4kv.V4KV_DEV_OVERFLOW
     assert torch.equal(d["out"], clean)
+    # offsets that decrease: nothing is attended
+    for cu in ([0, 9, 4], [3, 5, 2], [0, -1, 9]):
+        d = c.device()
+        d["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        c.run(d)
+        assert int(d["st"].item()) & v4kv.V4KV_DEV_OVERFLOW
+        assert (d["out"] == 7.0).all()
     # a top-k entry the sequence does not hold
     c = TreeCase(871, [900], [3], 64, topk=50)
     d = c.device()
@@ -586,6 +593,69 @@ def test_verify_edges():
     assert st == v4kv.V4KV_DEV_BAD_PROB and nxt[0] == -1 and n[0] == 1 and nxt[1] >= 0
     c = VerifyCase(946, [3], 40, shape="forest")
     assert list(c.check()) == [1]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_verify_takes_values_that_are_not_positive_as_zero(dtype):
+    for draft in (True, False):
+        c = VerifyCase(947, [9, 6, 30, 4], 211, dtype=dtype, draft=draft)
+        r = synth.rng(948)
+        for t in (c.target, c.draft)[:1 + draft]:
+            at = torch.from_numpy(r.random(tuple(t.shape)))
+            t[at < 0.3] *= -1.0
+            t[at > 0.9] = float("nan")
+        c.check()
+
+
+def test_verify_and_gather_captured_and_at_once():
+    """Replays with other values in the same buffers, and calls on two streams."""
+    from paged_compressed_kv_b200 import v4kv
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def prepare(c):
+        B, n = len(c.counts), c.N
+        t = dict(target=c.target.cuda(), draft=c.draft.cuda(), cu=torch.from_numpy(c.cu).cuda(),
+                 parents=torch.from_numpy(c.parents).cuda(), tokens=torch.from_numpy(c.tokens).cuda(),
+                 u=torch.from_numpy(c.u).cuda(), s=torch.from_numpy(c.s).cuda(), path=torch.zeros(B, c.max_nodes, **i32),
+                 n=torch.zeros(B, **i32), nxt=torch.zeros(B, **i32), x=torch.arange(n * 8.0, device="cuda").view(n, 8),
+                 gate=torch.arange(float(n), device="cuda"), cuo=torch.zeros(B + 1, **i32))
+        t["x"] = t["x"].to(torch.bfloat16)
+        t["xo"], t["go"] = torch.zeros_like(t["x"]), torch.zeros_like(t["gate"])
+        return t
+
+    def run(c, t, stream=None):
+        v4kv.v4kv_tree_verify(t["target"], t["cu"], t["parents"], t["tokens"], t["u"], t["s"], c.max_nodes, t["path"],
+                              t["n"], t["nxt"], draft=t["draft"], stream=stream)
+        v4kv.v4kv_tree_gather(t["x"], t["gate"], t["cu"], t["path"], t["n"], t["xo"], t["go"], t["cuo"], stream=stream)
+
+    outs = ("path", "n", "nxt", "xo", "go", "cuo")
+    cases = [VerifyCase(seed, [6] * 40, 5003) for seed in (970, 971)]
+    first, second = (prepare(c) for c in cases)
+    for c, t in zip(cases, (first, second)):
+        run(c, t)
+    want = [{k: t[k].clone() for k in outs} for t in (first, second)]
+    assert not torch.equal(want[0]["nxt"], want[1]["nxt"])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for t in (first, second):
+            for k in outs:
+                t[k].zero_()
+        torch.cuda.synchronize()
+        for c, t, s in zip(cases, (first, second), streams):
+            run(c, t, stream=s)
+        torch.cuda.synchronize()
+        for t, w in zip((first, second), want):
+            assert all(torch.equal(t[k], w[k]) for k in outs)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(cases[0], first)
+    for k in set(first) - set(outs):
+        first[k].copy_(second[k])
+    for k in outs:
+        first[k].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first[k], want[1][k]) for k in outs)
 
 
 # ------------------------------------------------------------------ packing and a whole step

@@ -111,6 +111,30 @@ def test_tree_attention_rejects(bad, status):
     assert _attend_status(**bad) == status
 
 
+@pytest.mark.parametrize("sizes", [
+    dict(total=1 << 28), dict(batch=1 << 24, window_len=1 << 10, max_len=1 << 20),
+    dict(batch=64, heads=128, total=8192, most=128, max_len=(1 << 31) - 1),
+    dict(batch=1 << 23, heads=128, total=1 << 23, most=128, max_len=0)])
+def test_tree_attention_refuses_sizes_it_cannot_count(sizes):
+    from paged_compressed_kv_b200 import v4kv
+    assert _attend_status(**sizes) == v4kv.V4KV_ERR_UNSUPPORTED
+    a = dict(batch=1, heads=8, total=4, most=4, max_len=1024, window_len=128)
+    a.update(sizes)
+    with pytest.raises(v4kv.V4KVError) as e:
+        v4kv.v4kv_tree_workspace_size(a["batch"], a["heads"], a["total"], a["most"], a["max_len"], 4, a["window_len"],
+                                      0, v4kv.V4KV_FP8_E4M3)
+    assert e.value.status == v4kv.V4KV_ERR_UNSUPPORTED
+
+
+def test_verify_takes_values_that_are_not_positive_as_zero():
+    nan = float("nan")
+    target = [[0.5, 0.5, 0.0], [1.0, 0.0, 0.0]]
+    # a draft's negative value or NaN at a token: accepted where the target has it, refused where not
+    for bad in (-1.0, nan):
+        assert tree.verify(target, [[0.5, bad, 0.5], [1, 0, 0]], [-1, 0], [0, 1], [0, 0.9], 0.0)[0] == [0, 1]
+        assert tree.verify(target, [[0.5, 0.5, bad], [1, 0, 0]], [-1, 0], [0, 2], [0, 0.9], 0.0)[0] == [0]
+
+
 def test_tree_attention_rejects_other_dims():
     from paged_compressed_kv_b200 import v4kv
     assert _attend_status(main=v4kv._Paged(FAKE, FAKE, 4, 64, 256, 1, FAKE, 4)) == 2
