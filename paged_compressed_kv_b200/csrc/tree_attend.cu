@@ -569,7 +569,7 @@ __device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& l
 // lane's two terms go: split in place.
 __device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
                                         uint8_t* lo_dst, float4* meta) {
-#pragma unroll 1
+#pragma unroll 2
   for (int r = r0; r < r0 + 8; ++r) {
     const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(r, lane & 7);
     uint4 raw[2], hi, lo;
@@ -603,7 +603,7 @@ __device__ __noinline__ uint32_t rows_seeing(uint32_t seen, const Unit& x, bool 
 #pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + 8 * j;
-#pragma unroll 1
+#pragma unroll
     for (int m = 0; m < 4; ++m) {
       bool v;
       if (entries) {
@@ -781,12 +781,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
           if (t.images == 1) {
             // rows from `safe` on are hidden from some of the unit's rows
             const int safe = max(0, min(32, x.n_all - t.first - 32 * w));
+            if (safe == 32) {  // no branch per row: 71 -> 67 us with 512 chosen entries a node
+              const unsigned long long mine = rows[32 * w + lane], none = reinterpret_cast<unsigned long long>(a.main.data);
+              const uint32_t d2 = d0 + (lane >> 3) * kChunk + 4096 * w;
 #pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-              const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[32 * w + r]);
-              const uint32_t off = (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7);
-              if (r < safe || !src)
-                cp_async16(d0 + off, src ? src + 16 * lane : static_cast<const uint8_t*>(a.main.data), src != nullptr);
+              for (int r = 0; r < 32; ++r) {
+                const unsigned long long src = __shfl_sync(0xffffffffu, mine, r);
+                cp_async16(d2 + tc::sw128_off(r, lane & 7), reinterpret_cast<const uint8_t*>(src ? src : none) + 16 * lane,
+                           src != 0);
+              }
+            } else {
+#pragma unroll 4
+              for (int r = 0; r < 32; ++r) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(rows[32 * w + r]);
+                if (r < safe || !src)
+                  cp_async16(d0 + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7),
+                             src ? src + 16 * lane : static_cast<const uint8_t*>(a.main.data), src != nullptr);
+              }
             }
             for (int r = safe; r < 32; ++r) {
               const uint4* src = reinterpret_cast<const uint4*>(rows[32 * w + r]);
@@ -1329,13 +1340,16 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     if (p.w.rec[k].x == p.w.rec[k + 1].x) continue;
     const size_t slot = 2 * (size_t)k + (p.w.rec[k].x < begin ? 1 : 0);
     const float2 ml = p.w.part_ml[slot * kR + row];
+    const float4* o = reinterpret_cast<const float4*>(p.w.part_o + (slot * kR + row) * kD);
+    float4 vv[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) vv[q] = o[32 * q + lane];
     const float nm = fmaxf(m, ml.x), f0 = exp2f(m - nm), f1 = exp2f(ml.x - nm);
     m = nm;
     l = l * f0 + ml.y * f1;
-    const float4* o = reinterpret_cast<const float4*>(p.w.part_o + (slot * kR + row) * kD);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 v = o[32 * q + lane];
+      const float4 v = vv[q];
       acc[4 * q] = acc[4 * q] * f0 + v.x * f1;
       acc[4 * q + 1] = acc[4 * q + 1] * f0 + v.y * f1;
       acc[4 * q + 2] = acc[4 * q + 2] * f0 + v.z * f1;
