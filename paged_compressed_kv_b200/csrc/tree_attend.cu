@@ -123,6 +123,7 @@ struct Params {
   int ratio_log, spb_log;  // of main_cache
   int hc;        // units per node (per_node)
   int per_node;  // a unit's rows belong to one node
+  int rope_blocks; // prep blocks per sequence for its nodes
   int raw_blocks;  // prep blocks per sequence for its raw rows
   int max_units;   // units of a sequence at most
   int boxes;     // tiles of entries that every node sees are loaded by TMA
@@ -1377,20 +1378,26 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   }
 }
 
-// Blocks b < batch: depths, ancestors and rotations of a sequence's nodes. Block
-// `batch`: the sequences' costs and the blocks' ranges. The others: raw rows (a
-// warp takes kPrepRows of a sequence) as two e4m3 terms, once for all units.
+// In order: blocks for the sequences' nodes (depths, ancestors, units, and 256 of
+// the rotations each: a tree of 128 nodes has 16 of them, 37 -> 32 us in all),
+// one for the sequences' costs and the grid's ranges, then those for raw rows (a
+// warp takes kPrepRows of a sequence) and for Q as two e4m3 terms, once for all
+// units, and for entries to be gathered.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ Params p) {
   tc::pdl_wait();
   tc::pdl_launch_dependents();
   const TreeArgs& a = p.a;
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (b < a.batch) {
+  const int trees = a.batch * p.rope_blocks;
+  if (b < trees) {
+    // block `part` of a sequence: 256 of the nodes' rotations, and part 0 the rest
+    const int part = blockIdx.x / a.batch, b = blockIdx.x - part * a.batch;
+    int32_t* st = part == 0 ? a.dev_status : nullptr;
     __shared__ int parent[V4KV_MAX_TREE_NODES];
     __shared__ int depth[V4KV_MAX_TREE_NODES];
-    const TreeSeq s = tree_seq(a.cu_nodes, b, a.total_nodes, a.max_nodes, t == 0 ? a.dev_status : nullptr);
-    if (t == 0 && a.seq_lens[b] > a.max_len) flag(a.dev_status, V4KV_DEV_OVERFLOW);
-    if (t < s.n) parent[t] = tree_parent(a.parents, s.first, t, a.dev_status);
+    const TreeSeq s = tree_seq(a.cu_nodes, b, a.total_nodes, a.max_nodes, t == 0 ? st : nullptr);
+    if (t == 0 && a.seq_lens[b] > a.max_len) flag(st, V4KV_DEV_OVERFLOW);
+    if (t < s.n) parent[t] = tree_parent(a.parents, s.first, t, st);
     __syncthreads();
     if (t < s.n) {
       uint32_t m[4] = {0, 0, 0, 0};
@@ -1401,14 +1408,16 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
           if (i >> 5 == k) m[k] |= 1u << (i & 31);
         ++d;
       }
-      p.w.anc[s.first + t] = make_uint4(m[0], m[1], m[2], m[3]);
-      p.w.depth[s.first + t] = d;
+      if (part == 0) {
+        p.w.anc[s.first + t] = make_uint4(m[0], m[1], m[2], m[3]);
+        p.w.depth[s.first + t] = d;
+      }
       depth[t] = d;
     }
     __syncthreads();
     // the units, and behind the last one the next sequence's first
     const SeqPlan plan = plan_of(p, b, nullptr);
-    for (int u = t; u < plan.units; u += 256) {
+    for (int u = t; u < plan.units && part == 0; u += 256) {
       int next = unit_index(p, plan, b, u + 1);
       if (u + 1 == plan.units) {
         next = -1;
@@ -1420,7 +1429,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       unit_store(p, plan, b, u, depth, next);
     }
     const int L = seq_len(a, b), pairs = a.rope.rope_dim >> 1;
-    for (int k = t; k < s.n * pairs; k += 256) {
+    const int k = 256 * part + t;
+    if (k < s.n * pairs) {
       const int i = k / pairs;
       float c, sn;
       rope_cs(a.rope, k - i * pairs, (long long)L + depth[i], &c, &sn);
@@ -1428,7 +1438,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     }
     return;
   }
-  const int raw_end = a.batch + 1 + a.batch * p.raw_blocks, q_end = raw_end + 2 * a.batch * p.max_units;
+  const int raw_end = trees + 1 + a.batch * p.raw_blocks, q_end = raw_end + 2 * a.batch * p.max_units;
   if (b >= q_end) {
     // kStageRows entries a warp, of the whole tiles that every node sees
     const int per = p.staged / (8 * kStageRows), bb = (b - q_end) / per;
@@ -1520,11 +1530,11 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     }
     return;
   }
-  if (b > a.batch) {
-    const int per = p.raw_blocks, bb = (b - a.batch - 1) / per;
+  if (b > trees) {
+    const int per = p.raw_blocks, bb = (b - trees - 1) / per;
     const SeqPlan q = plan_of(p, bb, nullptr);
     const int w0 = raw_w0(a, q), n_win = q.L - w0, n = q.s.n > 0 ? n_win + q.s.n : 0;
-    const int r0 = ((b - a.batch - 1) % per * 8 + warp) * kPrepRows;
+    const int r0 = ((b - trees - 1) % per * 8 + warp) * kPrepRows;
     const bool fp8 = a.window.dtype == V4KV_FP8_E4M3;
     const size_t base = raw_row0(a, q, bb);
     uint4 raw[kPrepRows][2];
@@ -1707,7 +1717,7 @@ bool tree_sizes_ok(int batch, int heads, int total_nodes, int max_nodes, int k, 
   const long long te = ((k > 0 ? k : max(0LL, (long long)max_len + max_nodes - window_len) / ratio) + kT - 1) / kT;
   const long long raw = min((long long)max_len, window_len - 1LL) + max_nodes;
   if (units * (te + (raw + kT - 1) / kT) > most) return false;
-  return batch * (2 + raw / (8 * kPrepRows) + 1 + 2LL * units_per_seq(heads, max_nodes, k)) +
+  return batch * (2 + max_nodes + raw / (8 * kPrepRows) + 2LL * units_per_seq(heads, max_nodes, k)) +
              (1LL << 21) / (8 * kStageRows) < most;
 }
 
@@ -1726,6 +1736,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   p.max_units = units_per_seq(a.heads, a.max_nodes, a.topk ? a.k : 0);
   p.ratio_log = a.ratio == 4 ? 2 : 7;
   p.spb_log = 8 - p.ratio_log;
+  p.rope_blocks = max(1, (a.max_nodes * (a.rope.rope_dim >> 1) + 255) / 256);
   p.raw_blocks = (min(a.window_len - 1, a.max_len) + a.max_nodes + 8 * kPrepRows - 1) / (8 * kPrepRows);
   p.staged = staged_rows(a.batch, a.heads, a.max_nodes, a.topk ? a.k : 0, a.window_len, a.max_len, a.ratio, a.main.dtype);
   layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.heads, a.total_nodes, a.topk ? a.k : 0, a.window_len,
@@ -1744,7 +1755,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_prep_kernel, dim3(a.batch + 1 + a.batch * (p.raw_blocks + 2 * p.max_units + p.staged / (8 * kStageRows))), dim3(256), 0, stream, p);
+  e = launch_pdl(tree_prep_kernel, dim3(1 + a.batch * (p.rope_blocks + p.raw_blocks + 2 * p.max_units + p.staged / (8 * kStageRows))), dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_attend_kernel, dim3(p.grid), dim3(kThreads), kSmemBytes, stream, p);
   if (e != cudaSuccess) return e;
