@@ -158,7 +158,11 @@ __device__ __forceinline__ int unit_index(const Params& p, const SeqPlan& q, int
   return p.per_node ? q.s.first * p.hc + u : b + (int)((long long)q.s.first * p.a.heads / kR) + u;
 }
 
-constexpr int kCostFp8 = 4, kCostTwo = 8, kCostSeg = 4;
+// Costs of a tile of fp8 entries, of a tile of two images and of a unit, in about
+// 540 cycles. They balance the blocks, and were fitted: against 8, 16 and 8
+// (the images' bytes) 64 sequences of 4K to 64K tokens take 727 us, not 752, and 32
+// of 128K to 1M tokens at ratio 128 take 370, not 385; small calls are as before.
+constexpr int kCostFp8 = 8, kCostTwo = 22, kCostSeg = 16;
 
 __device__ __forceinline__ SeqPlan plan_of(const Params& p, int b, int32_t* st) {
   const TreeArgs& a = p.a;
