@@ -36,11 +36,25 @@
 // kernel has written every Q as the image its products read, and every raw row
 // as its two terms, once for all units that use it.
 //
+// Loads: fp8 entries that every node sees come as TMA boxes of 64 rows (pages of
+// ratio 4, or rows that the prep kernel gathered: staged_rows), other rows by
+// 16-byte asynchronous copies. A row of 512 bytes a request would suit neither:
+// a TMA instruction takes about 50 cycles whatever it brings.
+//
 // Schedule: the tiles of all units are one list; the prep kernel gives each
 // block of the grid (one per SM) an equal share by estimated cost. A block that
 // runs all tiles of a unit writes its output, any other leaves a partial result
 // (O, m, l) that the merge kernel joins: a long context with few rows is split
 // over the whole GPU.
+//
+// Measured (work is 2 x 2 x 512 flops per node, head and item): 64 sequences of
+// 4K to 64K tokens, 8 nodes, 64 heads 727 us, 810 TFLOP/s; one of 131001 tokens with 31
+// nodes 163 us, 820 TFLOP/s. A tile takes 4300 cycles: 3200 of them are its
+// operands and its own 64 KB at 128 bytes a cycle, the rest is the part of the
+// softmax that the next scores do not cover. Small calls take 28 to 32 us, the
+// latency of three dependent launches with code that each block runs once; the
+// loops are kept short for that, and in steady state too: unrolled ones lost 3 to 8
+// percent to instruction fetch.
 #include "tc.cuh"
 #include "tree.cuh"
 

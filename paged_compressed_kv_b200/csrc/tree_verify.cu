@@ -11,10 +11,13 @@
 // reads one value of p and q, all of them fetched up front.
 //
 // Bound: one row of p (and of q, where a draft was refused) per sequence, 4
-// bytes a value, from HBM; for few sequences the latency of the walk and of the
-// exchange between blocks. A cluster of 8 blocks takes each sequence, an eighth
-// of the vocabulary each, so that a single sequence's row is fetched by 8 SMs at
-// once, all of a warp's loads in flight together; the partial sums cross through
+// bytes a value, from HBM: 5 us for 33 MB. In fact the chain of a sequence: the
+// launch, the walk, a row's fetch and its exchange between blocks, once for each
+// refused draft that has a sibling and once for the draw. Measured: 7.8 us for one
+// chain of 5 nodes and 32001 values, 29 us for 32 trees and 131072 values, 17 us
+// for 64 trees of guesses. A cluster of 8 blocks takes each sequence, an eighth of
+// the vocabulary each, so that a single sequence's row is fetched by 8 SMs at once,
+// all of a warp's loads in flight together; the partial sums cross through
 // distributed shared memory. Sums are fp64: with 10^5 values whose prefix sum is
 // compared with a given number, fp32 sums would change the drawn token for about
 // one draw in a hundred.
@@ -102,6 +105,7 @@ __device__ __forceinline__ double warp_sum_d(double v) {
 struct VerifyShared {
   double part[2][kCluster];   // the blocks' sums (each block writes its slot in all blocks)
   double warp_part[kVWarps];
+  double sub_part[kVWarps];   // of the run that the draw falls in
   float p[V4KV_MAX_TREE_NODES], q[V4KV_MAX_TREE_NODES], u[V4KV_MAX_TREE_NODES];
   int parent[V4KV_MAX_TREE_NODES], token[V4KV_MAX_TREE_NODES];
   int gone[V4KV_MAX_TREE_NODES];
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(kVThreads, 2)
     if (fine && rank == owner) {
       int w_own = -1;
       double start = before, run = before;
+#pragma unroll 1
       for (int w = 0; w < kVWarps && (w_own < 0 || run <= target); ++w) {
         if (sh.warp_part[w] > 0.0) {
           w_own = w;
@@ -309,26 +314,63 @@ __global__ void __launch_bounds__(kVThreads, 2)
         }
         run += sh.warp_part[w];
       }
-      if (warp == w_own) {
+      // Of a long run each warp sums a part again, and the draw goes on in the part
+      // that the target falls in: in one warp's hands the run takes up to 16 steps
+      // (64 sequences of 131072 values 24 us, 17 so; with runs of 2 steps, of 32001
+      // values, it would be 7.8 and 9.5).
+      const int own_id = rank * kVWarps + w_own;
+      const int o0 = min(r.groups, own_id * per), o1 = min(r.groups, o0 + per);
+      int w_sub = w_own, s0 = o0, s1 = o1;
+      bool head = own_id == 0, tail = own_id == nc * kVWarps - 1;
+      if (o1 - o0 > 64) {
+        const int sub = (o1 - o0 + kVWarps - 1) / kVWarps;
+        s0 = min(o1, o0 + warp * sub);
+        s1 = min(o1, s0 + sub);
+        head = head && warp == 0;
+        tail = tail && warp == kVWarps - 1;
+        odd = head && lane < r.head ? lane : tail && lane >= 4 && back + lane - 4 < r.vocab ? back + lane - 4 : -1;
+        double sum = odd >= 0 ? r.at(odd) : 0.0;
+#pragma unroll 1
+        for (int g = s0 + lane; g < s1; g += 32) {
+          const float4 pv = four_at(r.p + r.head + 4 * (size_t)g);
+          float4 qv = pv;
+          if (r.q) qv = four_at(r.q + r.head + 4 * (size_t)g);
+          sum += r.group_sum(g, pv, qv, r.q != nullptr);
+        }
+        sum = warp_sum_d(sum);
+        if (lane == 0) sh.sub_part[warp] = sum;
+        __syncthreads();
+        w_sub = -1;
+        run = start;
+#pragma unroll 1
+        for (int w = 0; w < kVWarps && (w_sub < 0 || run <= target); ++w) {
+          if (sh.sub_part[w] > 0.0) {
+            w_sub = w;
+            start = run;
+          }
+          run += sh.sub_part[w];
+        }
+      }
+      if (warp == w_sub) {
         // 32 groups at a time: their prefix sums over the lanes, then the group
         // that ends above the target. The row's first values come before the
         // first step, its last ones after the last.
         int found = -1, last = -1;
         run = start;
-        const int steps = (g1 - g0 + 31) / 32;
+        const int steps = (s1 - s0 + 31) / 32;
         float4 pn = make_float4(0.f, 0.f, 0.f, 0.f), qn = pn;
         auto fetch = [&](int i) {
           if (i < 0 || i >= steps) return;
-          const size_t e = r.head + 4 * (size_t)min(g0 + 32 * i + lane, g1 - 1);
+          const size_t e = r.head + 4 * (size_t)min(s0 + 32 * i + lane, s1 - 1);
           pn = four_at(r.p + e);
           if (r.q) qn = four_at(r.q + e);
         };
         fetch(0);
 #pragma unroll 1
-        for (int i = -1; i <= steps && found < 0; ++i) {
-          const int g = g0 + 32 * i + lane;
+        for (int i = head ? -1 : 0; i < steps + tail && found < 0; ++i) {
+          const int g = s0 + 32 * i + lane;
           const bool inner = i >= 0 && i < steps;
-          const bool mine = inner ? g < g1 : odd >= 0 && (odd < r.head) == (i < 0);
+          const bool mine = inner ? g < s1 : odd >= 0 && (odd < r.head) == (i < 0);
           const int first = inner ? r.head + 4 * g : odd;
           double w[4] = {0.0, 0.0, 0.0, 0.0};
           if (inner) {
@@ -386,7 +428,8 @@ __global__ void __launch_bounds__(kVThreads, 2)
 // v4kv_tree_gather. grid (batch, ceil(max_nodes / kGWarps)), a warp per path
 // position: the accepted rows are a few KB each, so the kernel is one launch
 // latency plus one chain of loads (path index, row). Every block sums the
-// counts of the sequences before its own itself, which saves a launch.
+// counts of the sequences before its own itself, which saves a launch: 4.2 us for
+// one sequence as for 128.
 namespace {
 constexpr int kGWarps = 8;
 }
@@ -435,8 +478,8 @@ __global__ void __launch_bounds__(kGWarps * 32) tree_gather_kernel(GatherArgs a)
 
 // Blocks per sequence: 8 while the batch then fits the GPU at two blocks per SM
 // (one sequence's row is fetched by 8 SMs), 4 or 2 for larger ones, so that one
-// wave does. 64 sequences, 131072 values: 26.8 us at 8 blocks (two waves),
-// 24.0 us at 4.
+// wave does. 64 sequences, 131072 values: 25.0 us at 8 blocks (two waves),
+// 16.6 us at 4.
 cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream) {
   int nc = kCluster;
   while (nc > 2 && (long long)a.batch * nc > 2LL * num_sms) nc /= 2;

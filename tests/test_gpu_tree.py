@@ -596,6 +596,23 @@ def test_verify_edges():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch", [3, 90])
+def test_verify_draws_at_the_ends_of_long_rows(batch, dtype):
+    """Numbers at the ends of the unit interval, and rows whose mass is in a few
+    values at the ends, the middle and behind a refused guess."""
+    V = 65539
+    c = VerifyCase(949, [2] * batch, V, dtype=dtype, draft=False, shape="chain")
+    c.u[:], c.s[:] = 1.0 - 2.0 ** -24, np.tile([0.0, 0.5, 1.0 - 2.0 ** -24], batch // 3)
+    c.check()
+    c.target[:] = 0.0
+    for i, at in enumerate([[0], [V - 1], [0, V - 1], [1, 2, V - 3], [V // 2], [0, V // 3, V - 2]]):
+        c.target[i, at] = torch.tensor([0.5, 0.25, 0.25][:len(at)], dtype=dtype)
+    c.target[6:] = c.target[:6].repeat(batch // 3, 1)[:2 * batch - 6]
+    c.tokens[:] = V - 1
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_verify_takes_values_that_are_not_positive_as_zero(dtype):
     for draft in (True, False):
         c = VerifyCase(947, [9, 6, 30, 4], 211, dtype=dtype, draft=draft)
