@@ -419,7 +419,8 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  *               aligned; contents need not be initialised
  * Sizes whose rows or tiles of 128 items do not count in 31 bits are refused
  * with V4KV_ERR_UNSUPPORTED. max_seq_len sets the work that may be planned and,
- * at ratio 128, up to 4.2 bytes of workspace per token and sequence.
+ * at ratio 128 or with bf16 entries, up to 1.1 GB of the workspace (a copy of the
+ * entries: 528 or 1040 bytes each).
  * Everything else, and a node with nothing to attend to (zeros), is as in
  * v4kv_decode_attention.
  */

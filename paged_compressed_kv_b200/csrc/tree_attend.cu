@@ -36,7 +36,7 @@
 // kernel has written every Q as the image its products read, and every raw row
 // as its two terms, once for all units that use it.
 //
-// Loads: fp8 entries that every node sees come as TMA boxes of 64 rows (pages of
+// Loads: entries that every node sees come as TMA boxes of 64 rows (fp8 pages of
 // ratio 4, or rows that the prep kernel gathered: staged_rows), other rows by
 // 16-byte asynchronous copies. A row of 512 bytes a request would suit neither:
 // a TMA instruction takes about 50 cycles whatever it brings.
@@ -121,7 +121,7 @@ struct TreeWs {
   int4* units;        // [images][4] Unit's fields
   uint8_t* raw;       // rows of the windows and trees as two e4m3 terms, 512 bytes each
   float2* raw_meta;   // their {scale, 0 or -inf: no such row}
-  uint8_t* ent;       // entries gathered from pages of two (staged), 512 bytes each
+  uint8_t* ent;       // gathered entries (staged): 512 bytes each, or two e4m3 terms of a bf16 one
   float4* ent_meta;   // their item_meta
   long long* cost;    // [batch + 1] prefix sums over sequences
   int32_t* tiles;     // [batch + 1]
@@ -143,7 +143,7 @@ struct Params {
   int boxes;     // tiles of entries that every node sees are loaded by TMA
   int staged;    // entries of a sequence in w.ent, 0: the boxes are pages
   const uint8_t* box_data;  // what they are taken from, and its rows
-  int box_rows;
+  int box_rows, box_bytes;
   CUtensorMap map;  // boxes of 64 rows x 128 bytes of box_data
 };
 
@@ -485,7 +485,7 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
   if (box_tile(p, x, t)) {
     if (p.staged) {
       const size_t row = (size_t)x.b * p.staged + t.first;
-      if (lane < 2) rows[64 * lane] = reinterpret_cast<unsigned long long>(p.w.ent) + (row + 64 * lane) * kD;
+      if (lane < 2) rows[64 * lane] = reinterpret_cast<unsigned long long>(p.w.ent) + (row + 64 * lane) * p.box_bytes;
 #pragma unroll
       for (int r = 0; r < 4; ++r) meta[lane + 32 * r] = p.w.ent_meta[row + lane + 32 * r];
       return;
@@ -770,21 +770,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             // a page that is missing is read behind the pool's end: zeros
-            y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(p.box_data)) / kD)
+            y[k] = rows[64 * k] ? (int)((rows[64 * k] - reinterpret_cast<unsigned long long>(p.box_data)) / p.box_bytes)
                                 : p.box_rows;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            if ((c & 1) == 0) ok = __all_sync(0xffffffffu, ok && wait_empty(im, c >> 1));
+          for (int n = 0; n < 4 * t.images; ++n) {  // 128 bytes of the rows
+            const int c = n & 3;
+            const uint32_t m = im + (n >> 2), at = m & 1;
+            if ((c & 1) == 0) ok = __all_sync(0xffffffffu, ok && wait_empty(m, c >> 1));
             if (!ok) break;
             if (lane == 0) {
               if (w > 0) {
-                tc::mbar_arrive(&bars->kv_full[s][c]);
+                tc::mbar_arrive(&bars->kv_full[at][c]);
               } else {
-                tc::mbar_arrive_expect_tx(&bars->kv_full[s][c], kChunk);
+                tc::mbar_arrive_expect_tx(&bars->kv_full[at][c], kChunk);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                  tc::tma_load_2d(sbase + kVOff + s * kStage + c * kChunk + k * (kChunk / 2), &p.map, 128 * c, y[k],
-                                  &bars->kv_full[s][c]);
+                  tc::tma_load_2d(sbase + kVOff + at * kStage + c * kChunk + k * (kChunk / 2), &p.map, 128 * n, y[k],
+                                  &bars->kv_full[at][c]);
               }
             }
           }
@@ -1057,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
       const Tile t = tile_of(p, x);
       const bool seg_last = x.tile + 1 == x.te + x.tr || i + 1 == n_tiles;
       if (t.count > 0) {
-        if (t.images == 2 && t.entries) {
+        if (t.images == 2 && t.entries && !box_tile(p, x, t)) {
           // bf16 entries: eight rows a warp
           ok = tc::mbar_wait(&bars->raw_full, split & 1, abort_flag);
           if (named_or(bar, !ok)) {
@@ -1472,7 +1474,27 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       const int pg = page_of(pool.block_table + (size_t)bb * pool.max_blocks, pool.max_blocks, j0 + lane, pool.spb,
                              pool.num_pages, a.dev_status);
       if (pg >= 0) slot = pg * pool.spb + (j0 + lane) % pool.spb;
-      p.w.ent_meta[row + lane] = item_meta(pg >= 0 ? pool.scales[slot] : 0.f, pg >= 0);
+      if (pool.dtype == V4KV_FP8_E4M3) p.w.ent_meta[row + lane] = item_meta(pg >= 0 ? pool.scales[slot] : 0.f, pg >= 0);
+    }
+    if (pool.dtype == V4KV_BF16) {
+      uint4 v[kStageRows][2];
+#pragma unroll
+      for (int k = 0; k < kStageRows; ++k) {
+        const int at = __shfl_sync(0xffffffffu, slot, k);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool.data) + (size_t)max(at, 0) * (2 * kD));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[k][e] = at >= 0 ? src[2 * lane + e] : make_uint4(0, 0, 0, 0);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.w.ent + row * (2 * kD)) + lane;
+#pragma unroll
+      for (int k = 0; k < kStageRows; ++k) {
+        uint4 hi, lo;
+        const float scale = split_row(v[k], hi, lo);
+        dst[k * (2 * kD / 16)] = hi;
+        dst[k * (2 * kD / 16) + kD / 16] = lo;
+        if (lane == k) p.w.ent_meta[row + k] = item_meta(scale, slot >= 0);
+      }
+      return;
     }
     uint4 v[kStageRows];
 #pragma unroll
@@ -1679,21 +1701,29 @@ int units_per_seq(int heads, int max_nodes, int k) {
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Entries per sequence that the prep kernel copies to consecutive rows, in whole
-// tiles, or 0. At ratio 128 a page has two entries, and a tile's 128 rows come
-// by 16-byte asynchronous copies, 6100 cycles against 3200 of products; copied
-// once, they come by TMA boxes as pages of 64 do. Every unit of a sequence reads
-// them again, so the copy has to be shared: with 32 sequences of 128K to 1M
-// tokens it gives 382 us against 428 for 16 units each, but 132 against 129 for
+// tiles, or 0. What is copied comes by TMA boxes of 64 rows, as pages of 64 do;
+// every unit of a sequence reads it, so the copy has to be shared.
+// fp8 at ratio 128: a page has two entries, and a tile's 128 rows come by 16-byte
+// asynchronous copies, 6100 cycles against 3200 of products. With 32 sequences of
+// 128K to 1M tokens 382 us against 428 for 16 units each, but 132 against 129 for
 // four and 74 against 57 for one.
+// bf16: the copy is split into its two terms, which the sweep does again for
+// every unit (11000 cycles a tile). 42 sequences of 65K to 844K tokens at ratio 128:
+// 425 us against 777 for six units each, 205 against 281 for two. Where each
+// block has a tile or less it only adds a step: one sequence of 2000 tokens and
+// four units 37 against 35 us, of 9000 47 against 46, of 20000 66 against 73.
 int staged_rows(int batch, int heads, int max_nodes, int k, int window_len, int max_len, int ratio, int main_dtype) {
-  if (ratio != 128 || k > 0 || main_dtype != V4KV_FP8_E4M3) return 0;
-  if (units_per_seq(heads, max_nodes, k) < 6) return 0;
+  const bool two = main_dtype != V4KV_FP8_E4M3;
+  if ((ratio != 128 && !two) || k > 0) return 0;
+  const int units = units_per_seq(heads, max_nodes, k);
+  if (units < (two ? 2 : 6)) return 0;
   const long long n = max(0LL, max_len + 1LL - window_len) / ratio / kT * kT;
-  return batch * n <= (1LL << 21) ? (int)n : 0;  // at most 1.1 GB
+  if (two && (long long)batch * units < 16 && n < 4096) return 0;
+  return batch * n <= (two ? 1LL << 20 : 1LL << 21) ? (int)n : 0;  // at most 1.1 GB
 }
 
 size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, int k, int window_len,
-              int max_len, int grid, int staged) {
+              int max_len, int grid, int staged, int main_dtype) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* r = base ? base + at : nullptr;
@@ -1713,7 +1743,7 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
   const size_t raws = (size_t)batch * (window_len - 1 < max_len ? window_len - 1 : max_len) + total_nodes;
   x.raw = take(raws * 2 * kD);
   x.raw_meta = reinterpret_cast<float2*>(take(raws * sizeof(float2)));
-  x.ent = take((size_t)batch * staged * kD);
+  x.ent = take((size_t)batch * staged * (main_dtype == V4KV_FP8_E4M3 ? kD : 2 * kD));
   x.ent_meta = reinterpret_cast<float4*>(take((size_t)batch * staged * sizeof(float4)));
   x.cost = reinterpret_cast<long long*>(take(((size_t)batch + 1) * 8));
   x.tiles = reinterpret_cast<int32_t*>(take(((size_t)batch + 1) * 4));
@@ -1742,7 +1772,7 @@ bool tree_sizes_ok(int batch, int heads, int total_nodes, int max_nodes, int k, 
 size_t tree_workspace_bytes(int batch, int heads, int total_nodes, int max_nodes, int k, int window_len, int max_len,
                             int ratio, int main_dtype, int num_sms) {
   return layout(nullptr, nullptr, batch, heads, total_nodes, k, window_len, max_len, num_sms,
-                staged_rows(batch, heads, max_nodes, k, window_len, max_len, ratio, main_dtype));
+                staged_rows(batch, heads, max_nodes, k, window_len, max_len, ratio, main_dtype), main_dtype);
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sms, cudaStream_t stream) {
@@ -1758,7 +1788,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   p.raw_blocks = (min(a.window_len - 1, a.max_len) + a.max_nodes + 8 * kPrepRows - 1) / (8 * kPrepRows);
   p.staged = staged_rows(a.batch, a.heads, a.max_nodes, a.topk ? a.k : 0, a.window_len, a.max_len, a.ratio, a.main.dtype);
   layout(&p.w, static_cast<uint8_t*>(workspace), a.batch, a.heads, a.total_nodes, a.topk ? a.k : 0, a.window_len,
-         a.max_len, p.grid, p.staged);
+         a.max_len, p.grid, p.staged, a.main.dtype);
   cudaError_t e = cudaSuccess;
   const bool pages = a.topk == nullptr && a.main.dtype == V4KV_FP8_E4M3 && a.main.spb == 64 &&
                      (long long)a.main.num_pages * 64 < (1LL << 30) &&
@@ -1767,7 +1797,8 @@ cudaError_t launch_tree_attention(const TreeArgs& a, void* workspace, int num_sm
   if (p.boxes) {
     p.box_data = p.staged ? p.w.ent : static_cast<const uint8_t*>(a.main.data);
     p.box_rows = p.staged ? a.batch * p.staged : a.main.num_pages * 64;
-    e = encode_cols_u8(&p.map, p.box_data, (uint64_t)p.box_rows, kD, 128, 64);
+    p.box_bytes = a.main.dtype == V4KV_FP8_E4M3 ? kD : 2 * kD;
+    e = encode_cols_u8(&p.map, p.box_data, (uint64_t)p.box_rows, p.box_bytes, 128, 64);
     if (e != cudaSuccess) return e;
   }
   e = cudaFuncSetAttribute(tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

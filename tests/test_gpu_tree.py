@@ -378,6 +378,32 @@ def test_missing_pages_and_scales_of_any_value(lens, counts, ratio, missing):
         assert (np.abs(out[i] - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("lens,counts,ratio,missing", [
+    ([3000, 700, 140], [8, 3, 1], 4, 3), ([3000, 700, 140], [8, 3, 1], 4, 11),
+    ([3000, 700, 140], [2, 2, 1], 4, 3), ([70000, 33000, 16600], [8, 3, 1], 128, 100)])
+def test_missing_pages_and_infinities_of_bf16_entries(lens, counts, ratio, missing):
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(879 + missing, lens, counts, 64, ratio=ratio, main_dtype="bf16")
+    d = c.device()
+    d["main"].block_table[0, missing] = -1
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_PAGE
+    out = d["out"].float().cpu().numpy().astype(np.float64)
+    n = counts[0]
+    for i in range(n):
+        ref, mass = without(c, 0, i, missing)
+        tol = (2.0 ** -9 + 2.0 ** -11) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max()
+        assert (np.abs(out[i] - ref) <= tol).all()
+    # an infinity, and a NaN, in an entry that every node sees
+    clean = d["out"].clone()
+    spb = 256 // ratio
+    d["main"].data[int(c.main.bt[0, 1]), spb - 1, 9] = float("inf")
+    d["main"].data[int(c.main.bt[1, 0]), spb - 1, 77] = float("nan")
+    c.run(d)
+    assert torch.isnan(d["out"][:n, :, 9]).all() and torch.isnan(d["out"][n:n + counts[1], :, 77]).all()
+    assert torch.equal(d["out"][n + counts[1]:], clean[n + counts[1]:])
+
+
 def test_scales_at_any_address():
     """Entry scales that begin 4, 8 and 12 bytes behind a 16-byte boundary."""
     c = TreeCase(876, [3000, 517], [5, 3], 64)
