@@ -473,6 +473,7 @@ v4kv_status v4kv_tree_workspace_size(int32_t batch, int32_t heads, int32_t total
   if (max_nodes < 1 || max_nodes > V4KV_MAX_TREE_NODES || window_len < max_nodes) return V4KV_ERR_INVALID_ARG;
   if (heads < 1 || heads > 128) return V4KV_ERR_UNSUPPORTED;
   if ((ratio != 4 && ratio != 128) || k > 2048) return V4KV_ERR_INVALID_ARG;
+  if (main_dtype != V4KV_FP8_E4M3 && main_dtype != V4KV_BF16) return V4KV_ERR_INVALID_ARG;
   if (!tree_sizes_ok(batch, heads, total_nodes, max_nodes, k, window_len, max_seq_len, ratio))
     return V4KV_ERR_UNSUPPORTED;
   int sms = 0;

@@ -136,7 +136,7 @@ struct Params {
   int grid;
   int ratio_log, spb_log;  // of main_cache
   int hc;        // units per node (per_node)
-  int per_node;  // a unit's rows belong to one node
+  int per_node;  // a unit's rows belong to one node: own top-k, or as 64 heads fill it; then only its ancestors are listed, and nothing is masked
   int rope_blocks; // prep blocks per sequence for its nodes
   int raw_blocks;  // prep blocks per sequence for its raw rows
   int max_units;   // units of a sequence at most

@@ -126,6 +126,19 @@ def test_tree_attention_refuses_sizes_it_cannot_count(sizes):
     assert e.value.status == v4kv.V4KV_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("bad", [
+    dict(batch=0), dict(total=-1), dict(most=0), dict(most=129), dict(window_len=3), dict(max_len=-1), dict(k=2049),
+    dict(k=-1), dict(ratio=8), dict(dtype=2), dict(dtype=9)])
+def test_tree_workspace_size_rejects(bad):
+    from paged_compressed_kv_b200 import v4kv
+    a = dict(batch=1, heads=8, total=4, most=4, max_len=1024, ratio=4, window_len=128, k=0, dtype=v4kv.V4KV_FP8_E4M3)
+    a.update(bad)
+    with pytest.raises(v4kv.V4KVError) as e:
+        v4kv.v4kv_tree_workspace_size(a["batch"], a["heads"], a["total"], a["most"], a["max_len"], a["ratio"],
+                                      a["window_len"], a["k"], a["dtype"])
+    assert e.value.status == v4kv.V4KV_ERR_INVALID_ARG
+
+
 def test_verify_takes_values_that_are_not_positive_as_zero():
     nan = float("nan")
     target = [[0.5, 0.5, 0.0], [1.0, 0.0, 0.0]]
