@@ -14,7 +14,7 @@
 // bytes a value, from HBM: 5 us for 33 MB. In fact the chain of a sequence: the
 // launch, the walk, a row's fetch and its exchange between blocks, once for each
 // refused draft that has a sibling and once for the draw. Measured: 7.8 us for one
-// chain of 5 nodes and 32001 values, 29 us for 32 trees and 131072 values, 17 us
+// chain of 5 nodes and 32001 values, 27 us for 32 trees and 131072 values, 16 us
 // for 64 trees of guesses. A cluster of 8 blocks takes each sequence, an eighth of
 // the vocabulary each, so that a single sequence's row is fetched by 8 SMs at once,
 // all of a warp's loads in flight together; the partial sums cross through
@@ -306,7 +306,6 @@ __global__ void __launch_bounds__(kVThreads, 2)
     if (fine && rank == owner) {
       int w_own = -1;
       double start = before, run = before;
-#pragma unroll 1
       for (int w = 0; w < kVWarps && (w_own < 0 || run <= target); ++w) {
         if (sh.warp_part[w] > 0.0) {
           w_own = w;
@@ -314,42 +313,34 @@ __global__ void __launch_bounds__(kVThreads, 2)
         }
         run += sh.warp_part[w];
       }
-      // Of a long run each warp sums a part again, and the draw goes on in the part
-      // that the target falls in: in one warp's hands the run takes up to 16 steps
-      // (64 sequences of 131072 values 24 us, 17 so; with runs of 2 steps, of 32001
-      // values, it would be 7.8 and 9.5).
+      // Each warp sums a part of the run again, and the draw goes on in the part that
+      // the target falls in: in one warp's hands a run takes up to 16 steps (64
+      // sequences of 131072 values 22.3 us, 15.5 so; 7.3 and 7.8 for one of 32001).
       const int own_id = rank * kVWarps + w_own;
       const int o0 = min(r.groups, own_id * per), o1 = min(r.groups, o0 + per);
-      int w_sub = w_own, s0 = o0, s1 = o1;
-      bool head = own_id == 0, tail = own_id == nc * kVWarps - 1;
-      if (o1 - o0 > 64) {
-        const int sub = (o1 - o0 + kVWarps - 1) / kVWarps;
-        s0 = min(o1, o0 + warp * sub);
-        s1 = min(o1, s0 + sub);
-        head = head && warp == 0;
-        tail = tail && warp == kVWarps - 1;
-        odd = head && lane < r.head ? lane : tail && lane >= 4 && back + lane - 4 < r.vocab ? back + lane - 4 : -1;
-        double sum = odd >= 0 ? r.at(odd) : 0.0;
+      const int sub = (o1 - o0 + kVWarps - 1) / kVWarps;
+      const int s0 = min(o1, o0 + warp * sub), s1 = min(o1, s0 + sub);
+      const bool head = own_id == 0 && warp == 0, tail = own_id == nc * kVWarps - 1 && warp == kVWarps - 1;
+      odd = head && lane < r.head ? lane : tail && lane >= 4 && back + lane - 4 < r.vocab ? back + lane - 4 : -1;
+      double sum = odd >= 0 ? r.at(odd) : 0.0;
 #pragma unroll 1
-        for (int g = s0 + lane; g < s1; g += 32) {
-          const float4 pv = four_at(r.p + r.head + 4 * (size_t)g);
-          float4 qv = pv;
-          if (r.q) qv = four_at(r.q + r.head + 4 * (size_t)g);
-          sum += r.group_sum(g, pv, qv, r.q != nullptr);
+      for (int g = s0 + lane; g < s1; g += 32) {
+        const float4 pv = four_at(r.p + r.head + 4 * (size_t)g);
+        float4 qv = pv;
+        if (r.q) qv = four_at(r.q + r.head + 4 * (size_t)g);
+        sum += r.group_sum(g, pv, qv, r.q != nullptr);
+      }
+      sum = warp_sum_d(sum);
+      if (lane == 0) sh.sub_part[warp] = sum;
+      __syncthreads();
+      int w_sub = -1;
+      run = start;
+      for (int w = 0; w < kVWarps && (w_sub < 0 || run <= target); ++w) {
+        if (sh.sub_part[w] > 0.0) {
+          w_sub = w;
+          start = run;
         }
-        sum = warp_sum_d(sum);
-        if (lane == 0) sh.sub_part[warp] = sum;
-        __syncthreads();
-        w_sub = -1;
-        run = start;
-#pragma unroll 1
-        for (int w = 0; w < kVWarps && (w_sub < 0 || run <= target); ++w) {
-          if (sh.sub_part[w] > 0.0) {
-            w_sub = w;
-            start = run;
-          }
-          run += sh.sub_part[w];
-        }
+        run += sh.sub_part[w];
       }
       if (warp == w_sub) {
         // 32 groups at a time: their prefix sums over the lanes, then the group
@@ -479,7 +470,7 @@ __global__ void __launch_bounds__(kGWarps * 32) tree_gather_kernel(GatherArgs a)
 // Blocks per sequence: 8 while the batch then fits the GPU at two blocks per SM
 // (one sequence's row is fetched by 8 SMs), 4 or 2 for larger ones, so that one
 // wave does. 64 sequences, 131072 values: 25.0 us at 8 blocks (two waves),
-// 16.6 us at 4.
+// 16 us at 4.
 cudaError_t launch_tree_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream) {
   int nc = kCluster;
   while (nc > 2 && (long long)a.batch * nc > 2LL * num_sms) nc /= 2;

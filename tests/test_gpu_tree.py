@@ -421,6 +421,33 @@ def test_scales_at_any_address():
     assert int(d["st"].item()) == 0
 
 
+@pytest.mark.parametrize("extra", [{}, dict(topk=200), dict(main_dtype="bf16"), dict(main_dtype="bf16", topk=200),
+                                   dict(ratio=128)])
+def test_pools_beyond_four_gigabytes(extra):
+    """The same rows at the end of pools whose byte offsets do not fit 32 bits."""
+    c = TreeCase(891, [2600, 700] if "ratio" not in extra else [30000, 17000], [7, 3], 64, **extra)
+    d = c.device()
+    c.run(d)
+    clean = d["out"].clone()
+    for name in ("main", "win"):
+        pool = d[name]
+        pages, page = pool.data.shape[0], pool.data[0].numel() * pool.data.element_size()
+        more = (1 << 32) // page + 100
+        data = torch.empty((more + pages,) + tuple(pool.data.shape[1:]), dtype=pool.data.dtype, device="cuda")
+        data[more:] = pool.data
+        pool.data = data
+        if pool.scales is not None:
+            scales = torch.empty(more + pages, pool.scales.shape[1], device="cuda")
+            scales[more:] = pool.scales
+            pool.scales = scales
+        pool.block_table = torch.where(pool.block_table >= 0, pool.block_table + more, pool.block_table)
+    d["out"].fill_(7.0)
+    c.run(d)
+    torch.cuda.synchronize()
+    assert int(d["st"].item()) == 0
+    assert torch.equal(d["out"], clean)
+
+
 def test_graphs_that_share_a_workspace():
     """Two captured calls of different sequences with one workspace, replayed in turn."""
     c, e = TreeCase(877, [2000, 300], [6, 2], 64), TreeCase(878, [17000], [8], 64, ratio=128)
