@@ -374,10 +374,10 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  * All three calls describe the trees the same way:
  *   cu_nodes    device int32 [batch + 1], non-decreasing from 0: sequence b's
  *               nodes are rows cu_nodes[b] .. cu_nodes[b+1] of every per-node
- *               array (rows behind cu_nodes[batch] are neither read nor written)
+ *               array (rows behind cu_nodes[batch] are neither read nor written).
+ *               v4kv_tree_attention flags offsets that decrease with
+ *               V4KV_DEV_OVERFLOW and leaves out as it was
  *   total_nodes host: rows of the per-node arrays
- *               (v4kv_tree_attention flags cu_nodes that decrease with
- *               V4KV_DEV_OVERFLOW and leaves out as it was)
  *   max_nodes   host bound of a sequence's nodes, 1 .. V4KV_MAX_TREE_NODES; the
  *               nodes of a longer sequence beyond it are left out and flagged
  *               V4KV_DEV_OVERFLOW

@@ -227,6 +227,22 @@ def test_rows_that_are_not_attended_may_hold_anything(main_dtype, win_dtype):
                 assert torch.equal(dirty["out"][row], clean["out"][row])
 
 
+@pytest.mark.parametrize("heads,q_fp32", [(64, False), (10, True)])
+def test_a_query_that_is_not_finite_reaches_its_own_row_only(heads, q_fp32):
+    c = TreeCase(864, [1500, 400], [4, 3], heads)
+    d = c.device(q_fp32=q_fp32)
+    c.run(d)
+    clean = d["out"].clone()
+    bad = [(1, 3, 100, float("nan")), (2, 0, 0, float("inf")), (6, heads - 1, 511, -float("inf"))]
+    for node, head, dim, value in bad:
+        d["q"][node, head, dim] = value
+    c.run(d)
+    for node, head, _, _ in bad:
+        assert torch.isnan(d["out"][node, head]).all()
+        d["out"][node, head] = clean[node, head]
+    assert torch.equal(d["out"], clean)
+
+
 def test_entries_visible_to_the_deeper_nodes_only():
     """Entries that only the deeper nodes of a chain see hold NaN codes."""
     c = TreeCase(861, [1027], [14], 64, shape="chain")
