@@ -117,6 +117,12 @@ struct VerifyShared {
 
 enum { kSumRow = 0, kDraw = 1 };
 
+// The cluster barrier in two halves: a block's shared memory may be written from
+// another one only once it is known to run, which every block says at entry and
+// asks before its first such write, with the walk in between.
+__device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_all_here() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 }  // namespace
 
 // A cluster of blocks per sequence, grid (blocks x batch). The code is kept short
@@ -129,11 +135,13 @@ __global__ void __launch_bounds__(kVThreads, 2)
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / nc;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster_here();
   tc::pdl_wait();
   tc::pdl_launch_dependents();
   int32_t* st = rank == 0 ? a.dev_status : nullptr;
   const TreeSeq s = tree_seq(a.cu_nodes, b, a.total_nodes, a.max_nodes, tid == 0 ? st : nullptr);
   if (s.n <= 0) {  // the whole cluster leaves
+    cluster_all_here();
     if (rank == 0) {
       for (int i = tid; i < a.max_nodes; i += kVThreads) a.path_out[(size_t)b * a.max_nodes + i] = -1;
       if (tid == 0) {
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(kVThreads, 2)
       sum = warp_sum_d(sum);
       if (lane == 0) sh.warp_part[warp] = sum;
       __syncthreads();
+      if (exchange == 0) cluster_all_here();
       // Two tables in turn: a block writes a table again two exchanges later,
       // behind a barrier that every block reached after reading it.
       double* part = sh.part[exchange & 1];

@@ -744,6 +744,22 @@ def test_verify_and_gather_captured_and_at_once():
     assert all(torch.equal(first[k], want[1][k]) for k in outs)
 
 
+@pytest.mark.parametrize("batch", [5, 40, 90])  # clusters of 8, 4 and 2 blocks
+def test_verify_while_its_blocks_start_apart(batch):
+    """Blocks of a cluster start as a busy GPU frees their places, and some
+    clusters leave at once: every repeat gives the oracle's tokens."""
+    c = VerifyCase(960 + batch, [7, 0, 5, 1, 0][:5] * (batch // 5), 4099)
+    busy, side = torch.randn(4096, 4096, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                busy.sum(dim=1)
+                busy.square()
+        c.check()
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ packing and a whole step
 
 @pytest.mark.parametrize("dim,per_channel", [(8, False), (512, False), (512, True), (1024, True), (200, True)])
