@@ -1174,6 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         if (__any_sync(0xffffffffu, high) && lane == 0) raise[done & 1] = 1;
         // the last tile's product has read P and its scales
         if (im > 0) ok = ok && tc::mbar_wait(&bars->kv_empty[(im - 1) & 1][1], ((im - 1) >> 1) & 1, abort_flag);
+        tc::tc_fence_after();  // O and P's scales are read and written below
         if (!__all_sync(0xffffffffu, ok) && lane == 0) {
           *abort_flag = 1;
           raise[done & 1] = 2;

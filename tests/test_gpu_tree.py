@@ -293,6 +293,34 @@ def test_scores_that_grow_along_the_context():
         assert (np.abs(out[i] - ref) <= tol).all()
 
 
+def test_references_that_rise_in_every_tile():
+    """Scores that pass the running reference in each of twelve tiles: O, sums and
+    scales are raised between the products, with the same bits in every run."""
+    c = TreeCase(866, [6000], [9], 64)
+    direction = np.sign(c.q[:, :1].mean(axis=(0, 1)))
+    c.q = codecs.bf16_round(np.broadcast_to(direction[None, None], c.q.shape) * (1 + 0.01 * c.q))
+    flat = codecs.e4m3_decode(c.main.data) * c.main.scales[..., None]
+    for j in range(1500):
+        page = int(c.main.bt[0, j // 64])
+        flat[page, j % 64] = 0.02 * flat[page, j % 64] + direction * 0.02 * j
+    codes, scales = codecs.quantize_entry(flat.reshape(-1, 512).astype(np.float32))
+    c.main.data[:] = codes.reshape(c.main.data.shape)
+    c.main.scales[:] = scales.reshape(c.main.scales.shape)
+    d = c.device()
+    c.run(d)
+    first = d["out"].clone()
+    out = first.float().cpu().numpy()
+    for i in (0, 4, 8):
+        ref, mass = c.oracle(0, i)
+        # scores reach 680 here: their fp32 sums are off by up to 512 * 680 * 2^-24
+        tol = (2.0 ** -9 + 2 * 512 * 680 * 2.0 ** -24) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max()
+        assert (np.abs(out[i] - ref) <= tol).all()
+    for _ in range(30):
+        d["out"].fill_(7.0)
+        c.run(d)
+        assert torch.equal(d["out"], first)
+
+
 def test_bad_inputs_are_flagged_and_skipped():
     from paged_compressed_kv_b200 import v4kv
     c = TreeCase(870, [900, 700], [5, 4], 64)
