@@ -472,8 +472,9 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
           }
           n += x.raw_tree;
         }
-        at = reinterpret_cast<unsigned long long>(p.w.raw) + (size_t)n * (2 * kD);
         mt = p.w.raw_meta[n];
+        // a row whose page is missing has not been written: zeros are taken for it
+        if (mt.y == 0.f) at = reinterpret_cast<unsigned long long>(p.w.raw) + (size_t)n * (2 * kD);
       }
       rows[k] = at;
       meta[k] = item_meta(mt.x, mt.y == 0.f);

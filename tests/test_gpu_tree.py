@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import synth
-from oracle import codecs, tree
+from oracle import attention, codecs, tree
+from oracle.rope import rope_rotate
 from tests.helpers import entry_rows, lay_out, window_rows
 
 pytestmark = pytest.mark.gpu
@@ -446,6 +447,40 @@ def test_missing_pages_and_infinities_of_bf16_entries(lens, counts, ratio, missi
     c.run(d)
     assert torch.isnan(d["out"][:n, :, 9]).all() and torch.isnan(d["out"][n:n + counts[1], :, 77]).all()
     assert torch.equal(d["out"][n + counts[1]:], clean[n + counts[1]:])
+
+
+@pytest.mark.parametrize("heads,win_dtype,missing", [(64, "bf16", 0), (64, "fp8", 1), (10, "bf16", 1), (10, "fp8", 0)])
+def test_missing_pages_of_the_window(heads, win_dtype, missing):
+    """The tokens of a window page that is not there are left out, whatever the
+    workspace held before; the other sequence is as it was."""
+    from paged_compressed_kv_b200 import v4kv
+    c = TreeCase(887 + heads, [300, 290], [4, 3], heads, win_dtype=win_dtype)
+    d = c.device()
+    c.run(d)
+    clean = d["out"].clone()
+    d["win"].block_table[0, missing] = -1
+    d["ws"] = c.workspace(d)
+    c.run(d)
+    assert int(d["st"].item()) == v4kv.V4KV_DEV_BAD_PAGE
+    assert torch.equal(d["out"][4:], clean[4:])
+    out = d["out"].float().cpu().numpy().astype(np.float64)
+    main, win = c.main.seq(0), c.win.seq(0)
+    for i in range(4):
+        fam = tree.family(c.parents[:4], i)
+        pos = 300 + len(fam) - 1
+        ents = list(range((pos + 1 - W) // 4))
+        toks = [t for t in range(pos + 1 - W, 300) if t // 256 != missing]
+        v = np.concatenate([c.k_tree[fam].astype(np.float64)] + [
+            attention.gather(p["data"], p["scales"], p["dtype"], p["block_table_row"], at)
+            for p, at in ((main, ents), (win, toks))])
+        s = c.q[i].astype(np.float64) @ v.T / math.sqrt(512)
+        w = np.exp(s - s.max(axis=1, keepdims=True))
+        w /= w.sum(axis=1, keepdims=True)
+        ref = rope_rotate(w @ v, pos, 1e6, 64, 448, inverse=True)
+        mass = w @ np.abs(v)
+        mass[:, 448:] = np.repeat(mass[:, 448:].reshape(heads, -1, 2).sum(axis=2), 2, axis=1)
+        tol = (2.0 ** -9 + 2.0 ** -11) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max()
+        assert (np.abs(out[i] - ref) <= tol).all()
 
 
 def test_scales_at_any_address():
