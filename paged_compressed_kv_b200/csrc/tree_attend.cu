@@ -122,7 +122,7 @@ struct TreeWs {
   uint8_t* raw;       // rows of the windows and trees as two e4m3 terms, 512 bytes each
   float2* raw_meta;   // their {scale, 0 or -inf: no such row}
   uint8_t* ent;       // gathered entries (staged): 512 bytes each, or two e4m3 terms of a bf16 one
-  float4* ent_meta;   // their item_meta
+  float2* ent_meta;   // their {scale, 0 or -inf: no such row}
   long long* cost;    // [batch + 1] prefix sums over sequences
   int32_t* tiles;     // [batch + 1]
   int4* rec;          // [grid + 1] a block's first tile: {index, its unit, -, tile in that}
@@ -433,14 +433,32 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 // ------------------------------------------------------------------ loading
 
 // what the softmax needs of an item: its scale, and for the weight of its raw
-// codes log2 |scale| and 1 / |scale|. A zero scale stands for zero codes (the
-// item still counts in the normaliser), one that is not finite for NaN.
-__device__ __forceinline__ float4 item_meta(float scale, bool there) {
+// codes log2 |scale| and 1 / |scale|. A scale that is not finite stands for NaN, a zero
+// scale for zero codes: the item has no value but counts in the normaliser, which is
+// summed as 2^(score + log2 |scale|) / |scale|. Any log2 does for it, and it gets one below
+// those of its block of 32 items (`top` is the largest of them, kNoTop if there is none):
+// near them, so that neither drives the other's power out of fp32, and 40 lower, so that
+// they keep their bits in P beside a row of zeros of up to 2^50 times their weight. It is
+// not below kLowest: a weight may reach 2^(kRaise + 8 - log2) of its reference, and a sum may
+// hold 2^21 of them.
+constexpr float kNoTop = 0.f, kBelow = 40.f, kLowest = -58.f;
+__device__ __forceinline__ float4 item_meta(float scale, bool there, float top) {
   if (!there) return make_float4(0.f, 0.f, 0.f, -INFINITY);
   if (!isfinite(scale)) return make_float4(__int_as_float(0x7fffffff), 0.f, 1.f, 0.f);
   const float m = fabsf(scale);
-  return m == 0.f ? make_float4(0.f, 0.f, 1.f, 0.f) : make_float4(scale, log2f(m), 1.f / m, 0.f);
+  if (m == 0.f) {
+    const float lg = fmaxf(top - kBelow, kLowest);
+    return make_float4(0.f, lg, exp2f(-lg), 0.f);
+  }
+  return make_float4(scale, log2f(m), 1.f / m, 0.f);
 }
+
+// floor(log2 |scale|) as far as it is of use to a block's other items
+__device__ __forceinline__ int scale_exponent(float scale, bool there) {
+  const int e = (int)(__float_as_uint(scale) >> 23 & 0xff);  // 0: zero or subnormal, 255: not finite
+  return there && e > 0 && e < 255 ? e - 127 : -128;
+}
+__device__ __forceinline__ float block_top(int e) { return e > -128 ? (float)e : kNoTop; }
 
 // Lane l resolves items l, l + 32, l + 64, l + 96 of a tile: their rows'
 // addresses (0: no such item) and scales. The loads go in phases (top-k entry,
@@ -477,7 +495,8 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
         if (mt.y == 0.f) at = reinterpret_cast<unsigned long long>(p.w.raw) + (size_t)n * (2 * kD);
       }
       rows[k] = at;
-      meta[k] = item_meta(mt.x, mt.y == 0.f);
+      const bool there = mt.y == 0.f;
+      meta[k] = item_meta(mt.x, there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(mt.x, there))));
     }
     return;
   }
@@ -488,7 +507,11 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
       const size_t row = (size_t)x.b * p.staged + t.first;
       if (lane < 2) rows[64 * lane] = reinterpret_cast<unsigned long long>(p.w.ent) + (row + 64 * lane) * p.box_bytes;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) meta[lane + 32 * r] = p.w.ent_meta[row + lane + 32 * r];
+      for (int r = 0; r < 4; ++r) {
+        const float2 mt = p.w.ent_meta[row + lane + 32 * r];
+        const bool there = mt.y == 0.f;
+        meta[lane + 32 * r] = item_meta(mt.x, there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(mt.x, there))));
+      }
       return;
     }
     // two whole pages: only their first rows' addresses are asked for
@@ -501,10 +524,15 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
     if ((lane & 15) == 0)
       rows[64 * (lane >> 4)] = there ? reinterpret_cast<unsigned long long>(pool.data) + slot * kD : 0;
     const float4 s4 = *reinterpret_cast<const float4*>(pool.scales + slot + 4 * (lane & 15));
-    meta[4 * lane] = item_meta(s4.x, there);
-    meta[4 * lane + 1] = item_meta(s4.y, there);
-    meta[4 * lane + 2] = item_meta(s4.z, there);
-    meta[4 * lane + 3] = item_meta(s4.w, there);
+    int e = max(max(scale_exponent(s4.x, there), scale_exponent(s4.y, there)),
+                max(scale_exponent(s4.z, there), scale_exponent(s4.w, there)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+    const float top = block_top(e);
+    meta[4 * lane] = item_meta(s4.x, there, top);
+    meta[4 * lane + 1] = item_meta(s4.y, there, top);
+    meta[4 * lane + 2] = item_meta(s4.z, there, top);
+    meta[4 * lane + 3] = item_meta(s4.w, there, top);
     return;
   }
   int j[4], pg[4], err = 0;
@@ -547,7 +575,9 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     rows[lane + 32 * r] = at[r];
-    meta[lane + 32 * r] = item_meta(scale[r], at[r] != 0);
+    const bool there = at[r] != 0;
+    meta[lane + 32 * r] =
+        item_meta(scale[r], there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(scale[r], there))));
   }
   if (err) flag(a.dev_status, err);
 }
@@ -571,8 +601,8 @@ __device__ __forceinline__ uint32_t amax_bf16(const uint4* r) {
   return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16;
 }
 
-// a lane's 16 dims of a bf16 row as two terms; the row's scale (NaN, and zero
-// terms, for a row that is not finite)
+// a lane's 16 dims of a bf16 row as two terms; the row's scale (0 for a row of
+// zeros; NaN, and zero terms, for a row that is not finite)
 __device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& lo) {
   const uint32_t m = amax_bf16(raw);
   if (m >= 0x7f800000u) {
@@ -582,11 +612,11 @@ __device__ __forceinline__ float split_row(const uint4* raw, uint4& hi, uint4& l
   float v[16];
   bf16x16(raw, v);
   split16(v, scale_up(m), hi, lo);
-  return scale_down(m);
+  return m == 0 ? 0.f : scale_down(m);
 }
 
 // Eight rows from r0 on whose 32 bytes of bf16 a lane were copied to where the
-// lane's two terms go: split in place.
+// lane's two terms go: split in place, and their scales put down.
 __device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, int lane, uint8_t* hi_dst,
                                         uint8_t* lo_dst, float4* meta) {
 #pragma unroll 2
@@ -596,7 +626,7 @@ __device__ __noinline__ void split_rows(const unsigned long long* rows, int r0, 
     raw[0] = *reinterpret_cast<uint4*>(hi_dst + off);
     raw[1] = *reinterpret_cast<uint4*>(lo_dst + off);
     const float scale = split_row(raw, hi, lo);
-    if (rows[r] && lane == 0) meta[r] = item_meta(scale, true);
+    if (rows[r] && lane == 0) meta[r].x = scale;
     *reinterpret_cast<uint4*>(hi_dst + off) = hi;
     *reinterpret_cast<uint4*>(lo_dst + off) = lo;
   }
@@ -827,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
               uint4 v = src[lane];
               if (__any_sync(0xffffffffu, has_nan_code(v))) {
                 v = make_uint4(0, 0, 0, 0);
-                if (lane == 0) mt[32 * w + r] = item_meta(__int_as_float(0x7fffffff), true);
+                if (lane == 0) mt[32 * w + r] = item_meta(__int_as_float(0x7fffffff), true, kNoTop);
               }
               *reinterpret_cast<uint4*>(dst + (lane >> 3) * kChunk + tc::sw128_off(32 * w + r, lane & 7)) = v;
             }
@@ -1073,7 +1103,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
                      sm + kVOff + s * kStage, sm + kVOff + (s ^ 1) * kStage, meta + slot * kT);
           tc::fence_proxy_async_smem();
           named_sync(bar);
-          if (w == 0 && lane < 8) tc::mbar_arrive(&bars->kv_full[lane >> 2][lane & 3]);
+          if (w == 0) {  // the block's 32 rows have been split
+            float4* mt = meta + slot * kT + 32 * qd + lane;
+            const float scale = mt->x;
+            const bool there = mt->w == 0.f;
+            *mt = item_meta(scale, there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(scale, there))));
+            __syncwarp();
+            if (lane < 8) tc::mbar_arrive(&bars->kv_full[lane >> 2][lane & 3]);
+          }
         }
         ok = tc::mbar_wait(&bars->s_full, done & 1, abort_flag);
         tc::tc_fence_after();
@@ -1476,7 +1513,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       const int pg = page_of(pool.block_table + (size_t)bb * pool.max_blocks, pool.max_blocks, j0 + lane, pool.spb,
                              pool.num_pages, a.dev_status);
       if (pg >= 0) slot = pg * pool.spb + (j0 + lane) % pool.spb;
-      if (pool.dtype == V4KV_FP8_E4M3) p.w.ent_meta[row + lane] = item_meta(pg >= 0 ? pool.scales[slot] : 0.f, pg >= 0);
+      if (pool.dtype == V4KV_FP8_E4M3)
+        p.w.ent_meta[row + lane] = pg >= 0 ? make_float2(pool.scales[slot], 0.f) : make_float2(0.f, -INFINITY);
     }
     if (pool.dtype == V4KV_BF16) {
       uint4 v[kStageRows][2];
@@ -1494,7 +1532,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
         const float scale = split_row(v[k], hi, lo);
         dst[k * (2 * kD / 16)] = hi;
         dst[k * (2 * kD / 16) + kD / 16] = lo;
-        if (lane == k) p.w.ent_meta[row + k] = item_meta(scale, slot >= 0);
+        if (lane == k) p.w.ent_meta[row + k] = make_float2(scale, slot >= 0 ? 0.f : -INFINITY);
       }
       return;
     }
@@ -1746,7 +1784,7 @@ size_t layout(TreeWs* w, uint8_t* base, int batch, int heads, int total_nodes, i
   x.raw = take(raws * 2 * kD);
   x.raw_meta = reinterpret_cast<float2*>(take(raws * sizeof(float2)));
   x.ent = take((size_t)batch * staged * (main_dtype == V4KV_FP8_E4M3 ? kD : 2 * kD));
-  x.ent_meta = reinterpret_cast<float4*>(take((size_t)batch * staged * sizeof(float4)));
+  x.ent_meta = reinterpret_cast<float2*>(take((size_t)batch * staged * sizeof(float2)));
   x.cost = reinterpret_cast<long long*>(take(((size_t)batch + 1) * 8));
   x.tiles = reinterpret_cast<int32_t*>(take(((size_t)batch + 1) * 4));
   x.rec = reinterpret_cast<int4*>(take(((size_t)grid + 1) * sizeof(int4)));

@@ -271,6 +271,96 @@ def test_scales_of_any_value():
     c.check(d["out"])
 
 
+def check_finite(c, d, nodes=None):
+    """TreeCase.check lets a NaN pass: it is not above a tolerance."""
+    assert torch.isfinite(d["out"][:int(c.cu[-1])].float()).all()
+    c.check(d["out"], nodes=nodes)
+
+
+@pytest.mark.parametrize("lens,counts,heads,extra", CASES)
+def test_outputs_of_ordinary_calls_are_finite(lens, counts, heads, extra):
+    c = TreeCase(802 + heads + lens[0], lens, counts, heads, **extra)
+    d = c.device()
+    c.run(d)
+    assert torch.isfinite(d["out"][:int(c.cu[-1])].float()).all()
+
+
+def scored(c, log2_score):
+    """Queries that give each node's own row this score."""
+    k = c.k_tree[:, None].astype(np.float64)
+    c.q = codecs.bf16_round(np.broadcast_to(k * (log2_score * math.log(2) * math.sqrt(512)) /
+                                            (k * k).sum(-1, keepdims=True), c.q.shape).astype(np.float32))
+
+
+@pytest.mark.parametrize("log2_score", [2, 7])
+@pytest.mark.parametrize("heads", [64, 6])
+def test_a_window_of_zeros_beside_a_drafted_token(heads, log2_score):
+    c = TreeCase(1000 + heads, [127, 40], [1, 3], heads)
+    c.win.data[:] = 0
+    c.k_tree = codecs.bf16_round(c.k_tree * 3)
+    scored(c, log2_score)
+    d = c.device()
+    c.run(d)
+    check_finite(c, d)
+
+
+def test_a_drafted_token_of_zeros_alone_in_its_block():
+    """96 ordinary tokens, then the node: its 32 items are its own row alone."""
+    c = TreeCase(1003, [96, 128, 31], [1, 2, 4], 64)
+    c.k_tree[[0, 2, 3]] = 0
+    d = c.device()
+    c.run(d)
+    check_finite(c, d)
+
+
+@pytest.mark.parametrize("lens,counts,extra", [
+    ([3000], [3], {}), ([3000, 900], [8, 8], {}), ([2600, 700], [3, 5], dict(topk=200)),
+    ([3000], [3], dict(main_dtype="fp8"))])
+@pytest.mark.parametrize("size", [2.0 ** -20, 1.0, 2.0 ** 6])
+def test_rows_of_zeros_beside_others(lens, counts, extra, size):
+    """Runs of zero rows of every kind, and single ones, beside small, ordinary
+    and large rows (scores stay below 8)."""
+    c = TreeCase(1010 + len(lens), lens, counts, 64, **dict(dict(main_dtype="bf16"), **extra))
+    r = synth.rng(11)
+    c.q = codecs.bf16_round(c.q * np.float32(1.0 / size))
+    c.k_tree = codecs.bf16_round(c.k_tree * np.float32(size))
+    c.win.data[:] = codecs.bf16_bits(codecs.bf16_to_f32(c.win.data) * np.float32(size))
+    if c.main.dtype == "bf16":
+        c.main.data[:] = codecs.bf16_bits(codecs.bf16_to_f32(c.main.data) * np.float32(size))
+        gone = c.main.data
+    else:
+        c.main.scales *= np.float32(size)
+        gone = c.main.scales
+    gone[1] = 0
+    gone[r.random(c.main.data.shape[:2]) < 0.2] = 0
+    c.win.data[r.random(c.win.data.shape[:2]) < 0.2] = 0
+    c.win.data[:, 40:120] = 0
+    c.k_tree[1::3] = 0
+    d = c.device()
+    c.run(d)
+    check_finite(c, d, nodes=chosen(c, synth.rng(2)))
+    assert int(d["st"].item()) == 0
+
+
+def test_nothing_but_zeros():
+    """An output of zeros, split over the blocks or not."""
+    c = TreeCase(1020, [9000, 90], [2, 3], 64, main_dtype="bf16")
+    c.main.data[:], c.win.data[:], c.k_tree[:] = 0, 0, 0
+    d = c.device()
+    c.run(d)
+    assert not d["out"].any()
+
+
+@pytest.mark.parametrize("heads", [64, 8])
+def test_zeros_in_a_long_context_that_blocks_share(heads):
+    """Partial results with and without zero rows are joined."""
+    c = TreeCase(1021, [40001], [3], heads, main_dtype="bf16")
+    c.main.data[synth.rng(12).random(c.main.data.shape[0]) < 0.3] = 0
+    d = c.device()
+    c.run(d)
+    check_finite(c, d)
+
+
 def test_scores_that_grow_along_the_context():
     """A query along one direction whose entries' magnitude grows: the running
     maximum rises again and again, by far more than any fixed range."""
