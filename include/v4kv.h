@@ -405,7 +405,10 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  * of at least 2^-13 A and within 2^-21 A below; an fp32 q is
  * rounded to such terms (relative 2^-9). Softmax weights are rounded to two
  * terms (relative 2^-9) with a power-of-two scale per 32 items; accumulation,
- * maxima and sums are fp32. Any fp8 scale is valid, zero and negative ones too.
+ * maxima and sums are fp32. Any fp8 scale is valid, zero and negative ones too;
+ * a row whose scale is below 2^-76, or 2^-60 of the largest of its tile's 32 rows,
+ * counts as zeros (a bf16 row's scale is 2^-7 of its largest magnitude, rounded down to
+ * a power of two). Rows of one node may differ by up to 2^100 in magnitude.
  * A row that is not attended never enters a result, whatever it holds; an
  * attended row with a NaN or an infinity makes the attending outputs NaN (at
  * least in the dims that hold it).

@@ -28,7 +28,7 @@
 //     precision next to a dominating one elsewhere. Without it a long tail of
 //     small weights would round to zero together.
 // The normaliser and the running reference are fp32. With block scales P needs
-// no fixed range, so the reference moves only when a score passes it by 2^40.
+// no fixed range, so the reference moves only when a score passes it by 2^20.
 //
 // Warps: 0-15 softmax (a thread has 4 items of the tile and 4 of the rows) and
 // the unit's epilogue, 16-19 load tiles, 20 issues the MMAs, 21 and 22 resolve
@@ -68,7 +68,7 @@ constexpr int kD = 512;
 constexpr int kThreads = 768;
 constexpr int kRing = 4;  // tiles whose rows are resolved ahead
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
-constexpr float kRaise = 40.f;   // log2 by which a score may pass its reference
+constexpr float kRaise = 20.f;   // log2 by which a score may pass its reference
 constexpr int kPairs = 256;     // rotated pairs of a row at most
 constexpr int kPrepRows = 4;    // rows a warp of the prep kernel splits
 constexpr int kStageRows = 8;   // entries it copies
@@ -435,28 +435,29 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 // what the softmax needs of an item: its scale, and for the weight of its raw
 // codes log2 |scale| and 1 / |scale|. A scale that is not finite stands for NaN, a zero
 // scale for zero codes: the item has no value but counts in the normaliser, which is
-// summed as 2^(score + log2 |scale|) / |scale|. Any log2 does for it, and it gets one below
+// summed as 2^(score + log2 |scale|) / |scale|. So is one taken whose scale is below
+// 2^kLowest, or 2^-kApart of the largest in its block of 32 items: there the power or the
+// quotient is not an fp32 value, while a weight of P's block carries 2^-21 of the largest
+// weight times scale. Any log2 does for an item without a value, and it gets one below
 // those of its block of 32 items (`top` is the largest of them, kNoTop if there is none):
 // near them, so that neither drives the other's power out of fp32, and 40 lower, so that
 // they keep their bits in P beside a row of zeros of up to 2^50 times their weight. It is
 // not below kLowest: a weight may reach 2^(kRaise + 8 - log2) of its reference, and a sum may
 // hold 2^21 of them.
-constexpr float kNoTop = 0.f, kBelow = 40.f, kLowest = -58.f;
+constexpr float kNoTop = 0.f, kBelow = 40.f, kLowest = -76.f, kApart = 60.f;
 __device__ __forceinline__ float4 item_meta(float scale, bool there, float top) {
   if (!there) return make_float4(0.f, 0.f, 0.f, -INFINITY);
   if (!isfinite(scale)) return make_float4(__int_as_float(0x7fffffff), 0.f, 1.f, 0.f);
-  const float m = fabsf(scale);
-  if (m == 0.f) {
-    const float lg = fmaxf(top - kBelow, kLowest);
-    return make_float4(0.f, lg, exp2f(-lg), 0.f);
-  }
-  return make_float4(scale, log2f(m), 1.f / m, 0.f);
+  const float m = fabsf(scale), l2 = log2f(m);
+  if (l2 >= fmaxf(top - kApart, kLowest)) return make_float4(scale, l2, 1.f / m, 0.f);
+  const float lg = fmaxf(top - kBelow, kLowest);
+  return make_float4(0.f, lg, exp2f(-lg), 0.f);
 }
 
-// floor(log2 |scale|) as far as it is of use to a block's other items
+// floor(log2 |scale|) of an item with a value
 __device__ __forceinline__ int scale_exponent(float scale, bool there) {
   const int e = (int)(__float_as_uint(scale) >> 23 & 0xff);  // 0: zero or subnormal, 255: not finite
-  return there && e > 0 && e < 255 ? e - 127 : -128;
+  return there && e >= 127 + (int)kLowest && e < 255 ? e - 127 : -128;
 }
 __device__ __forceinline__ float block_top(int e) { return e > -128 ? (float)e : kNoTop; }
 
@@ -1278,7 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const __grid_c
         if (lane == 0) tc::mbar_arrive(&bars->p_full);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          // 2^(ex - ref), an integer power below 2^41
+          // 2^(ex - ref), an integer power below 2^21
           const float d = fmaxf(ex[m] - ref[m], -127.f);
           l[m] = fmaf(lt[m], __int_as_float(((int)d + 127) << 23), l[m]);
         }

@@ -361,6 +361,92 @@ def test_zeros_in_a_long_context_that_blocks_share(heads):
     check_finite(c, d)
 
 
+def check_small(c, d):
+    """As TreeCase.check, with half a step of bf16's subnormal values, and with what rows
+    may hold that count as zeros: a scale below 2^-76 or 2^-60 of the largest. A bf16 row of
+    largest magnitude A has the scale 2^(floor(log2 A) - 7), so either kind's values are
+    below 2^9 scales."""
+    scales = [np.abs(p.scales.astype(np.float64)).ravel() if p.dtype == "fp8" else
+              np.abs(codecs.bf16_to_f32(p.data).astype(np.float64)).max(axis=-1).ravel() for p in (c.main, c.win)]
+    scales.append(np.abs(c.k_tree.astype(np.float64)).max(axis=-1))
+    for k, of_rows in enumerate((c.main.dtype == "bf16", c.win.dtype == "bf16", True)):
+        if of_rows:
+            _, e = np.frexp(scales[k])
+            scales[k] = np.where(scales[k] > 0, np.ldexp(1.0, e - 8), 0.0)
+    scales = np.concatenate(scales)
+    gone = scales[scales < max(2.0 ** -76, 2.0 ** -60 * scales.max())]
+    lost = 2.0 ** 9 * gone.max() if gone.size else 0.0
+    out = d["out"].float().cpu().numpy().astype(np.float64)
+    for b, n in enumerate(c.counts):
+        for i in range(n):
+            ref, mass = c.oracle(b, i)
+            tol = (2.0 ** -9 + 2.0 ** -11) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mass.max() + 2.0 ** -133 + lost
+            fine = np.abs(out[c.cu[b] + i] - ref) <= tol
+            assert fine.all(), (b, i, int((~fine).sum()))
+
+
+@pytest.mark.parametrize("power", [-149, -135, -127, -120, -100, -77, -76, -65, -50, -20])
+@pytest.mark.parametrize("lens,counts,extra", [([1500], [4], {}), ([40001], [2], dict(heads=8)),
+                                               ([2600, 700], [3, 5], dict(topk=200))])
+def test_fp8_scales_near_zero(lens, counts, extra, power):
+    """Entries that count in the normaliser and hardly or not in the value: all of them,
+    some of them, of either sign, down to the smallest fp32 number."""
+    c = TreeCase(1030, lens, counts, **dict(dict(heads=64), **extra))
+    r = synth.rng(13)
+    tiny = np.float32(2.0) ** power if power > -127 else np.ldexp(np.float32(1), power)
+    keep = c.main.scales.copy()
+    for some in (1.1, 0.5):
+        c.main.scales[:] = np.where(r.random(keep.shape) < some, tiny, keep)
+        c.main.scales[r.random(keep.shape) < 0.2] *= -1.0
+        d = c.device()
+        c.run(d)
+        check_small(c, d)
+
+
+def test_fp8_scales_of_all_sizes_at_once():
+    c = TreeCase(1031, [3000, 400], [5, 3], 64, win_dtype="fp8")
+    r = synth.rng(14)
+    for pool in (c.main, c.win):
+        powers = r.choice([-149, -140, -128, -126, -110, -80, -70, -45, -20, 0], pool.scales.shape)
+        pool.scales[:] = np.where(powers < 0, np.ldexp(np.float32(1), powers), pool.scales)
+        pool.scales[r.random(pool.scales.shape) < 0.1] = 0.0
+    d = c.device()
+    c.run(d)
+    check_small(c, d)
+
+
+@pytest.mark.parametrize("power", [-130, -118, -100, -68, -60, -36, 36, 60, 100])
+@pytest.mark.parametrize("main_dtype", ["bf16", "fp8"])
+def test_rows_of_any_magnitude(main_dtype, power):
+    """All rows near 2^power, with queries that keep the scores ordinary where
+    that is possible; then beside ordinary rows."""
+    c = TreeCase(1040, [1500, 300], [4, 3], 64, main_dtype=main_dtype)
+    size = np.ldexp(np.float64(1), power)
+
+    def sized(x):
+        return codecs.bf16_round((x.astype(np.float64) * size).astype(np.float32))
+
+    r = synth.rng(15)
+    q, win, main = c.q.copy(), c.win.data.copy(), c.main.data.copy()
+    scales = None if c.main.scales is None else c.main.scales.copy()
+    c.k_tree = sized(c.k_tree)
+    c.q = codecs.bf16_round((q / max(size, 2.0 ** -100)).astype(np.float32))
+    for some in (1.1, 0.5):
+        if some < 1:
+            c.q = codecs.bf16_round((q / max(size, 1.0)).astype(np.float32))
+        at = r.random(win.shape[:2])[..., None] < some
+        c.win.data[:] = np.where(at, codecs.bf16_bits(sized(codecs.bf16_to_f32(win))), win)
+        at = r.random(main.shape[:2]) < some
+        if scales is None:
+            c.main.data[:] = np.where(at[..., None], codecs.bf16_bits(sized(codecs.bf16_to_f32(main))), main)
+        else:
+            c.main.scales[:] = np.where(at, (scales.astype(np.float64) * size).astype(np.float32), scales)
+        d = c.device()
+        c.run(d)
+        check_small(c, d)
+        assert int(d["st"].item()) == 0
+
+
 def test_scores_that_grow_along_the_context():
     """A query along one direction whose entries' magnitude grows: the running
     maximum rises again and again, by far more than any fixed range."""
