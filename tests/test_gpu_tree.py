@@ -10,7 +10,7 @@ import torch
 import synth
 from oracle import attention, codecs, tree
 from oracle.rope import rope_rotate
-from tests.helpers import entry_rows, lay_out, window_rows
+from tests.helpers import entry_rows, lay_out, oracle_index, window_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -158,6 +158,34 @@ def test_attention_with_fp32_queries(heads, extra):
     d = c.device(q_fp32=True)
     c.run(d)
     c.check(d["out"], q_fp32=True)
+    assert int(d["st"].item()) == 0
+
+
+def two_terms(q, low=True):
+    """q as the products take it: hi + lo / 16, e4m3 both, of the row scaled so that
+    its largest magnitude is in [2^7, 2^8); the residual in half precision."""
+    up = np.exp2(7.0 - np.floor(np.log2(np.abs(q).max(axis=-1, keepdims=True)))).astype(np.float32)
+    x = (q * up).astype(np.float32)
+    hi = codecs.e4m3_decode(codecs.e4m3_encode(x)).astype(np.float16)
+    rest = ((x.astype(np.float16) - hi) * np.float16(16)).astype(np.float32)
+    lo = codecs.e4m3_decode(codecs.e4m3_encode(rest))
+    return (hi.astype(np.float64) + (lo / 16 if low else 0.0)) / up
+
+
+@pytest.mark.parametrize("heads,extra", [(64, {}), (8, dict(main_dtype="bf16")), (64, dict(topk=100))])
+def test_fp32_queries_are_held_in_two_terms(heads, extra):
+    """With q rounded as the header says, an output is within the bound of bf16
+    queries. The same bound does not hold for a q without its low terms."""
+    c = TreeCase(842, [1800, 333], [6, 3], heads, **extra)
+    c.q = synth.normal(synth.rng(843), c.q.shape)
+    d = c.device(q_fp32=True)
+    c.run(d)
+    q = c.q
+    c.q = two_terms(q)
+    c.check(d["out"])
+    c.q = two_terms(q, low=False)
+    with pytest.raises(AssertionError):
+        c.check(d["out"])
     assert int(d["st"].item()) == 0
 
 
@@ -445,6 +473,33 @@ def test_rows_of_any_magnitude(main_dtype, power):
         c.run(d)
         check_small(c, d)
         assert int(d["st"].item()) == 0
+
+
+def test_own_entries_chosen_by_the_indexer():
+    """v4kv_index_topk with a node per row, then the nodes' attention over what it chose."""
+    from paged_compressed_kv_b200 import v4kv
+    k = 48
+    c = TreeCase(1050, [900, 120, 133], [5, 2, 6], 64, topk=k)
+    r = synth.rng(1051)
+    keys = lay_out([codecs.quantize_entry(synth.normal(r, (-(-L // 4), 128))) for L in c.lens], 64, r, "fp8")
+    q_idx = synth.normal(r, (c.N, 128))
+    seq = np.repeat(np.arange(3), c.counts)
+    depth = [len(tree.family(c.parents[c.cu[b]:c.cu[b + 1]], n - c.cu[b])) - 1 for n, b in enumerate(seq)]
+    ends = [c.lens[b] + depth[n] + 1 for n, b in enumerate(seq)]
+    d = c.device()
+    pool = keys.to_cuda()
+    pool.block_table = pool.block_table[torch.from_numpy(seq).cuda()].contiguous()
+    n = v4kv.v4kv_workspace_size(v4kv.V4KV_OP_INDEX_TOPK, c.N, 1, max(ends), 4, W, k, v4kv.V4KV_FP8_E4M3, 128)
+    v4kv.v4kv_index_topk(torch.from_numpy(q_idx).cuda(), pool, torch.tensor(ends, dtype=torch.int32, device="cuda"),
+                         max(ends), 4, W, k, d["topk"], torch.empty(max(n, 256), dtype=torch.uint8, device="cuda"),
+                         dev_status=d["st"])
+    c.run(d)
+    assert int(d["st"].item()) == 0
+    c.topk = d["topk"].cpu().numpy()
+    for n, b in enumerate(seq):
+        assert np.array_equal(c.topk[n], oracle_index(q_idx[n], keys, b, ends[n], 4, W, k)[0])
+    assert (c.topk[5] >= 0).sum() < (c.topk[12] >= 0).sum() < k
+    c.check(d["out"])
 
 
 def test_scores_that_grow_along_the_context():
