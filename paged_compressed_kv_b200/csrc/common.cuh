@@ -24,6 +24,13 @@ __device__ __forceinline__ void flag(int32_t* st, int bit) {
   if (st) atomicOr(st, bit);
 }
 
+// 2^x on the special-function unit (ftz: results below 2^-126 become 0)
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- codecs
 // fp8-e4m3 pair -> f16 pair, exact (every e4m3 value is an f16 value).
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint16_t two) {

@@ -85,13 +85,6 @@ static_assert(sizeof(Bars) <= 256, "barrier area");
 constexpr uint32_t kInfoFp8 = 1;    // rows are fp8 codes (else bf16)
 constexpr uint32_t kInfoFirst = 2;  // first tile of a segment (new sequence)
 
-// 2^x on the special-function unit (ftz: results below 2^-126 become 0)
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
