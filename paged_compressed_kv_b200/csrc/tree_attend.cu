@@ -18,9 +18,13 @@
 //     MN-major A of the second from one copy. Nothing is converted, and an
 //     item costs 512 bytes, not 1024.
 //   - q and P are two e4m3 terms each, hi + lo / 16: four significant bits
-//     and four of what is left, 2^-9 of a value in all, half of bf16's
-//     rounding; a bf16 q is exact. Two fp8 products cost what one f16 product
-//     does. q's two terms are one N = 128 operand, so V is read once for both.
+//     and four of what is left, 2^-9 of a value (and 2^-11, split2), where bf16
+//     keeps 2^-8 and an f16 operand 2^-11; a bf16 q is exact. Two fp8 products
+//     cost what one f16 product does, but V need not be converted: a third term, or
+//     f16 operands, would cost half of the products again, or V's bytes twice. Against
+//     fp64 the outputs are off by 0.0017 to 0.0019 (relative, all of a case), the plain
+//     form in fp32 by 0.0017: the bf16 result. q's two terms are one N = 128 operand, so
+//     V is read once for both.
 //   - A bf16 row (window token, drafted token, bf16 entry) is two images hi and
 //     lo of the same kind, scaled by a power of two: two fp8 tiles.
 //   - e4m3 spans 2^-9 .. 448. P's terms carry a power-of-two scale for each row
@@ -47,11 +51,12 @@
 // (O, m, l) that the merge kernel joins: a long context with few rows is split
 // over the whole GPU.
 //
-// Measured (work is 2 x 2 x 512 flops per node, head and item): 64 sequences of
-// 4K to 64K tokens, 8 nodes, 64 heads 727 us, 810 TFLOP/s; one of 131001 tokens with 31
-// nodes 163 us, 820 TFLOP/s. A tile takes 4300 cycles: 3200 of them are its
-// operands and its own 64 KB at 128 bytes a cycle, the rest is the part of the
-// softmax that the next scores do not cover. Small calls take 28 to 32 us, the
+// Measured (work is 2 x 2 x 512 flops per node, head and item), in calls in a row: 64
+// sequences of 4K to 64K tokens, 8 nodes, 64 heads 868 us, 680 TFLOP/s, at the power
+// limit's clock (730 to 760 us in a short burst of graph replays); one of 131001 tokens
+// with 31 nodes 178 us, 750 TFLOP/s (163 to 170 in a burst). A tile takes 4300 cycles:
+// 3200 of them are its operands and its own 64 KB at 128 bytes a cycle, the rest is the
+// part of the softmax that the next scores do not cover. Small calls take 31 to 33 us, the
 // latency of three dependent launches with code that each block runs once; the
 // loops are kept short for that, and in steady state too: unrolled ones lost 3 to 8
 // percent to instruction fetch.
@@ -293,12 +298,6 @@ __device__ __forceinline__ bool box_tile(const Params& p, const Unit& x, const T
   return p.boxes && t.entries && t.first + kT <= seen_by_all(p, x.L);
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool named_or(int id, bool p) {
   uint32_t r;
@@ -338,7 +337,9 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   return r;
 }
 
-// two e4m3 terms of a pair: x = hi + lo / 16
+// Two e4m3 terms of a pair: x = hi + lo / 16. What is left of x is formed in half
+// precision, which rounds x by 2^-11 beside lo's 2^-9 (a bf16 value and the difference
+// are exact): fp32 takes twice the instructions, in the loop that bounds the sweep.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const uint16_t h = float2_to_e4m3x2(x, y);
   const __half2 r = __hmul2(__hsub2(__floats2half2_rn(x, y), e4m3x2_to_half2(h)), __float2half2_rn(16.f));
@@ -436,14 +437,15 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 // codes log2 |scale| and 1 / |scale|. A scale that is not finite stands for NaN, a zero
 // scale for zero codes: the item has no value but counts in the normaliser, which is
 // summed as 2^(score + log2 |scale|) / |scale|. So is one taken whose scale is below
-// 2^kLowest, or 2^-kApart of the largest in its block of 32 items: there the power or the
-// quotient is not an fp32 value, while a weight of P's block carries 2^-21 of the largest
-// weight times scale. Any log2 does for an item without a value, and it gets one below
-// those of its block of 32 items (`top` is the largest of them, kNoTop if there is none):
-// near them, so that neither drives the other's power out of fp32, and 40 lower, so that
-// they keep their bits in P beside a row of zeros of up to 2^50 times their weight. It is
-// not below kLowest: a weight may reach 2^(kRaise + 8 - log2) of its reference, and a sum may
-// hold 2^21 of them.
+// 2^kLowest, or 2^-kApart of the largest in its block of 32 items. Otherwise that sum could
+// leave fp32: a weight may reach 2^(kRaise + 8 - log2 |scale|) of the reference, and a sum may
+// hold 2^21 of them; and a weight of 2^-45 of the block's largest or more would lose its
+// power beside a scale that is larger still. P carries 2^-21 of a block's largest weight
+// times scale, so that such a value is far below its bits.
+// Any log2 does for an item without a value, and it gets one below those of its block
+// (`top` is the largest of them, kNoTop if there is none): near them, so that neither
+// drives the other's power out of fp32, and 40 lower, so that they keep their bits in P
+// beside a row of zeros of up to 2^50 times their weight, but not below kLowest.
 constexpr float kNoTop = 0.f, kBelow = 40.f, kLowest = -76.f, kApart = 60.f;
 __device__ __forceinline__ float4 item_meta(float scale, bool there, float top) {
   if (!there) return make_float4(0.f, 0.f, 0.f, -INFINITY);

@@ -13,9 +13,10 @@
 // Bound: one row of p (and of q, where a draft was refused) per sequence, 4
 // bytes a value, from HBM: 5 us for 33 MB. In fact the chain of a sequence: the
 // launch, the walk, a row's fetch and its exchange between blocks, once for each
-// refused draft that has a sibling and once for the draw. Measured: 7.8 us for one
-// chain of 5 nodes and 32001 values, 27 us for 32 trees and 131072 values, 16 us
-// for 64 trees of guesses. A cluster of 8 blocks takes each sequence, an eighth of
+// refused draft that has a sibling and once for the draw. Measured in calls in a row
+// (and as graph replays): 10.7 us (7.8) for one chain of 5 nodes and 32001 values, 28 us
+// (28) for 32 trees and 131072 values, 17 us (15.5) for 64 trees of guesses; bf16
+// probabilities take as long. A cluster of 8 blocks takes each sequence, an eighth of
 // the vocabulary each, so that a single sequence's row is fetched by 8 SMs at once,
 // all of a warp's loads in flight together; the partial sums cross through
 // distributed shared memory. Sums are fp64: with 10^5 values whose prefix sum is
@@ -428,8 +429,8 @@ __global__ void __launch_bounds__(kVThreads, 2)
 // v4kv_tree_gather. grid (batch, ceil(max_nodes / kGWarps)), a warp per path
 // position: the accepted rows are a few KB each, so the kernel is one launch
 // latency plus one chain of loads (path index, row). Every block sums the
-// counts of the sequences before its own itself, which saves a launch: 4.2 us for
-// one sequence as for 128.
+// counts of the sequences before its own itself, which saves a launch: 4.2 us in a
+// graph (9.3 as a call) for one sequence as for 128.
 namespace {
 constexpr int kGWarps = 8;
 }
