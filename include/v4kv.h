@@ -402,10 +402,12 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  * Numerics: every operand of the tensor cores is one or two fp8-e4m3 terms.
  * Cached codes are exact. A bf16 row (an entry, a window token, k_tree or q) is
  * split into two terms relative to its largest magnitude A, exact for values
- * of at least 2^-13 A and within 2^-21 A below; an fp32 q is
- * rounded to such terms (relative 2^-9). Softmax weights are rounded to two
- * terms (relative 2^-9) with a power-of-two scale per 32 items; accumulation,
- * maxima and sums are fp32. Any fp8 scale is valid, zero and negative ones too;
+ * of at least 2^-13 A and within 2^-21 A below; an fp32 q is rounded to such
+ * terms (relative 2^-9 + 2^-11). Softmax weights are rounded to two terms (the
+ * same) with a power-of-two scale per 32 items: of a weight times its row's scale
+ * that is below 2^-13 of the largest of them, 2^-21 of that largest is kept.
+ * Accumulation, maxima and sums are fp32. v4kv_decode_attention holds q and the
+ * weights in 2^-11. Any fp8 scale is valid, zero and negative ones too;
  * a row whose scale is below 2^-76, or 2^-60 of the largest of its tile's 32 rows,
  * counts as zeros (a bf16 row's scale is 2^-7 of its largest magnitude, rounded down to
  * a power of two). Rows of one node may differ by up to 2^100 in magnitude.
@@ -416,14 +418,18 @@ v4kv_status v4kv_decode_attention_noalloc(const void* q, int32_t q_dtype, int32_
  *               each node's position
  *   k_tree      device bf16 [total_nodes, dim], RoPE applied
  *   window_len  at least max_nodes, so that no drafted token leaves the window
- *   topk        device int32 [total_nodes, k] or NULL, k 1 .. 2048
+ *   topk        device int32 [total_nodes, k] or NULL, k 1 .. 2048.
+ *               v4kv_index_topk gives it with a node per row of its batch: q_idx
+ *               and seq_lens (L + depth + 1) per node, and the sequence's row of
+ *               idx_cache's block table repeated for each of its nodes (the keys
+ *               are then read once per node)
  *   out         device bf16 [total_nodes, heads, dim]
  *   workspace   device scratch of v4kv_tree_workspace_size bytes, 256-byte
  *               aligned; contents need not be initialised
  * Sizes whose rows or tiles of 128 items do not count in 31 bits are refused
  * with V4KV_ERR_UNSUPPORTED. max_seq_len sets the work that may be planned and,
  * at ratio 128 or with bf16 entries, up to 1.1 GB of the workspace (a copy of the
- * entries: 528 or 1040 bytes each).
+ * entries: 520 or 1032 bytes each).
  * Everything else, and a node with nothing to attend to (zeros), is as in
  * v4kv_decode_attention.
  */
