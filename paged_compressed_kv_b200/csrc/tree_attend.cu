@@ -463,6 +463,42 @@ __device__ __forceinline__ int scale_exponent(float scale, bool there) {
 }
 __device__ __forceinline__ float block_top(int e) { return e > -128 ? (float)e : kNoTop; }
 
+// An fp8 row of zeros has codes 0 and, as the compressor writes it, the scale 1: beside rows
+// of ordinary scales (2^-9) its weight would take their bits in P. So of a row whose
+// scale is 2^kWide or more above its block's smallest (`low`) the codes are looked at: a
+// row of zeros gets the scale 0. Nearly always 16 bytes settle it.
+constexpr int kWide = 4;
+__device__ __forceinline__ float scale_of_codes(float scale, unsigned long long row, int low) {
+  if (scale_exponent(scale, row != 0) < low + kWide) return scale;
+  const uint4* c = reinterpret_cast<const uint4*>(row);
+#pragma unroll 1
+  for (int k = 0; k < kD / 16; ++k) {
+    const uint4 v = c[k];
+    if ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) return scale;
+  }
+  return 0.f;
+}
+// (127: no item has a value)
+__device__ __forceinline__ int low_exponent(int e) { return e > -128 ? e : 127; }
+
+// Whether all of a tile's items have values, with scales within 2^kWide: then no item
+// stands out, and no block's largest is asked for (kAnyTop does). A lane gives four.
+constexpr float kAnyTop = -128.f;
+__device__ __forceinline__ bool alike(const float* s, bool a, bool b, bool c, bool d) {
+  const bool there[4] = {a, b, c, d};
+  int low = 127, high = -128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = scale_exponent(s[i], true);
+    if (there[i]) {
+      low = min(low, e);
+      high = max(high, e);
+    }
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  return low > -128 && __reduce_max_sync(0xffffffffu, high) < low + kWide;
+}
+
 // Lane l resolves items l, l + 32, l + 64, l + 96 of a tile: their rows'
 // addresses (0: no such item) and scales. The loads go in phases (top-k entry,
 // block table, scale), the four of a phase independent of one another.
@@ -509,12 +545,20 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
     if (p.staged) {
       const size_t row = (size_t)x.b * p.staged + t.first;
       if (lane < 2) rows[64 * lane] = reinterpret_cast<unsigned long long>(p.w.ent) + (row + 64 * lane) * p.box_bytes;
+      float scale[4], top[4] = {kAnyTop, kAnyTop, kAnyTop, kAnyTop};
+      bool there[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float2 mt = p.w.ent_meta[row + lane + 32 * r];
-        const bool there = mt.y == 0.f;
-        meta[lane + 32 * r] = item_meta(mt.x, there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(mt.x, there))));
+        scale[r] = mt.x;
+        there[r] = mt.y == 0.f;
       }
+      if (!alike(scale, there[0], there[1], there[2], there[3])) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top[r] = block_top(__reduce_max_sync(0xffffffffu, scale_exponent(scale[r], there[r])));
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) meta[lane + 32 * r] = item_meta(scale[r], there[r], top[r]);
       return;
     }
     // two whole pages: only their first rows' addresses are asked for
@@ -527,15 +571,25 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
     if ((lane & 15) == 0)
       rows[64 * (lane >> 4)] = there ? reinterpret_cast<unsigned long long>(pool.data) + slot * kD : 0;
     const float4 s4 = *reinterpret_cast<const float4*>(pool.scales + slot + 4 * (lane & 15));
-    int e = max(max(scale_exponent(s4.x, there), scale_exponent(s4.y, there)),
-                max(scale_exponent(s4.z, there), scale_exponent(s4.w, there)));
+    float scale[4] = {s4.x, s4.y, s4.z, s4.w}, top = kAnyTop;
+    if (!alike(scale, there, there, there, there)) {
+      int low = 127, e = -128;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-    const float top = block_top(e);
-    meta[4 * lane] = item_meta(s4.x, there, top);
-    meta[4 * lane + 1] = item_meta(s4.y, there, top);
-    meta[4 * lane + 2] = item_meta(s4.z, there, top);
-    meta[4 * lane + 3] = item_meta(s4.w, there, top);
+      for (int i = 0; i < 4; ++i) low = min(low, low_exponent(scale_exponent(scale[i], there)));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (there) scale[i] = scale_of_codes(scale[i], reinterpret_cast<unsigned long long>(pool.data) + (slot + 4 * (lane & 15) + i) * kD, low);
+        e = max(e, scale_exponent(scale[i], there));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+      top = block_top(e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) meta[4 * lane + i] = item_meta(scale[i], there, top);
     return;
   }
   int j[4], pg[4], err = 0;
@@ -575,12 +629,22 @@ __device__ __forceinline__ void resolve_tile(const Params& p, const Unit& x, con
       at[r] = reinterpret_cast<unsigned long long>(pool.data) + slot * (fp8 ? kD : 2 * kD);
     }
   }
+  float top[4] = {kAnyTop, kAnyTop, kAnyTop, kAnyTop};
+  if (!alike(scale, at[0] != 0, at[1] != 0, at[2] != 0, at[3] != 0)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool there = at[r] != 0;
+      if (fp8) {
+        scale[r] = scale_of_codes(scale[r], at[r], __reduce_min_sync(0xffffffffu, low_exponent(scale_exponent(scale[r], there))));
+        __syncwarp();
+      }
+      top[r] = block_top(__reduce_max_sync(0xffffffffu, scale_exponent(scale[r], there)));
+    }
+  }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     rows[lane + 32 * r] = at[r];
-    const bool there = at[r] != 0;
-    meta[lane + 32 * r] =
-        item_meta(scale[r], there, block_top(__reduce_max_sync(0xffffffffu, scale_exponent(scale[r], there))));
+    meta[lane + 32 * r] = item_meta(scale[r], at[r] != 0, top[r]);
   }
   if (err) flag(a.dev_status, err);
 }
@@ -1512,12 +1576,12 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
     const size_t row = (size_t)bb * p.staged + j0;
     const PoolArgs& pool = a.main;
     int slot = -1;
+    float kept = 0.f;
     if (lane < kStageRows) {
       const int pg = page_of(pool.block_table + (size_t)bb * pool.max_blocks, pool.max_blocks, j0 + lane, pool.spb,
                              pool.num_pages, a.dev_status);
       if (pg >= 0) slot = pg * pool.spb + (j0 + lane) % pool.spb;
-      if (pool.dtype == V4KV_FP8_E4M3)
-        p.w.ent_meta[row + lane] = pg >= 0 ? make_float2(pool.scales[slot], 0.f) : make_float2(0.f, -INFINITY);
+      if (pool.dtype == V4KV_FP8_E4M3 && slot >= 0) kept = pool.scales[slot];
     }
     if (pool.dtype == V4KV_BF16) {
       uint4 v[kStageRows][2];
@@ -1547,8 +1611,15 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       if (at >= 0) v[k] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool.data) + (size_t)at * kD)[lane];
     }
     uint4* dst = reinterpret_cast<uint4*>(p.w.ent + row * kD) + lane;
+    unsigned zeros = 0;
 #pragma unroll
-    for (int k = 0; k < kStageRows; ++k) dst[k * (kD / 16)] = v[k];
+    for (int k = 0; k < kStageRows; ++k) {
+      dst[k * (kD / 16)] = v[k];
+      if (!__any_sync(0xffffffffu, (v[k].x | v[k].y | v[k].z | v[k].w) & 0x7f7f7f7fu)) zeros |= 1u << k;
+    }
+    if (lane < kStageRows)
+      p.w.ent_meta[row + lane] = slot < 0 ? make_float2(0.f, -INFINITY)
+                                          : make_float2(zeros >> lane & 1 ? 0.f : kept, 0.f);
     return;
   }
   if (b >= raw_end) {
@@ -1659,6 +1730,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       } else if (__any_sync(0xffffffffu, has_nan_code(hi))) {
         hi = lo;
         scale[k] = __int_as_float(0x7fffffff);
+      } else if (!__any_sync(0xffffffffu, (hi.x | hi.y | hi.z | hi.w) & 0x7f7f7f7fu)) {
+        scale[k] = 0.f;  // a row of zeros
       }
       uint4* dst = reinterpret_cast<uint4*>(p.w.raw + (base + r0 + k) * (2 * kD));
       dst[lane] = hi;

@@ -370,6 +370,33 @@ def test_rows_of_zeros_beside_others(lens, counts, extra, size):
     assert int(d["st"].item()) == 0
 
 
+@pytest.mark.parametrize("lens,counts,extra", [
+    ([3000], [3], {}), ([3000, 900], [8, 8], dict(win_dtype="fp8")), ([2600, 700], [3, 5], dict(topk=200)),
+    ([900, 500], [3, 7], dict(heads=6)), ([40000, 33000], [8, 3], dict(ratio=128)), ([40000], [2], dict(ratio=128))])
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -12, 1.0])
+def test_fp8_rows_of_zero_codes(lens, counts, extra, size):
+    """Rows of zeros as the compressor writes them, codes 0 and the scale 1, beside
+    small and ordinary rows whose scales are far below it."""
+    c = TreeCase(1060 + len(lens), lens, counts, **dict(dict(heads=64), **extra))
+    r = synth.rng(16)
+    c.q = codecs.bf16_round(c.q * np.float32(1.0 / size))
+    c.k_tree = codecs.bf16_round(c.k_tree * np.float32(size))
+    for pool in (c.main, c.win):
+        if pool.dtype == "bf16":
+            pool.data[:] = codecs.bf16_bits(codecs.bf16_to_f32(pool.data) * np.float32(size))
+            continue
+        pool.scales *= np.float32(size)
+        gone = r.random(pool.scales.shape) < 0.2
+        gone[0] = True
+        gone[r.random(gone.shape) < 0.02] = True
+        pool.data[gone] = np.where(r.random((int(gone.sum()), 512)) < 0.5, 0x80, 0)  # either zero
+        pool.scales[gone] = 1.0
+    d = c.device()
+    c.run(d)
+    check_finite(c, d, nodes=chosen(c, synth.rng(2)))
+    assert int(d["st"].item()) == 0
+
+
 def test_nothing_but_zeros():
     """An output of zeros, split over the blocks or not."""
     c = TreeCase(1020, [9000, 90], [2, 3], 64, main_dtype="bf16")
