@@ -52,9 +52,9 @@
 // over the whole GPU.
 //
 // Measured (work is 2 x 2 x 512 flops per node, head and item), in calls in a row: 64
-// sequences of 4K to 64K tokens, 8 nodes, 64 heads 868 us, 680 TFLOP/s, at the power
+// sequences of 4K to 64K tokens, 8 nodes, 64 heads 870 to 890 us, 670 TFLOP/s, at the power
 // limit's clock (730 to 760 us in a short burst of graph replays); one of 131001 tokens
-// with 31 nodes 178 us, 750 TFLOP/s (163 to 170 in a burst). A tile takes 4300 cycles:
+// with 31 nodes 180 us, 740 TFLOP/s (168 to 171 in a burst). A tile takes 4300 cycles:
 // 3200 of them are its operands and its own 64 KB at 128 bytes a cycle, the rest is the
 // part of the softmax that the next scores do not cover. Small calls take 31 to 33 us, the
 // latency of three dependent launches with code that each block runs once; the
